@@ -18,6 +18,8 @@
 
 #include "../../include/kie.h"
 #include "kie_internal.h"
+#include "kie_kv4.h"
+#include "kie_sample.h"
 
 extern "C" void* kie_decode_kernel_ptr(int hd, int kv);
 extern "C" void* kie_decode_batch_kernel_ptr(int hd, int kv);
@@ -1761,6 +1763,194 @@ extern "C" kie_status kie_decode_step_static_scratch(kie_engine* e, int32_t toke
     // a device error of this step is reported by the engine's next synchronising call
     KIE_CUDA(e, kie_launch_err_merge(P.ctl, reinterpret_cast<KieControl*>(e->dev(e->lay.ctl)), e->stream));
     e->pos += 1;
+    return KIE_OK;
+}
+
+// ---- operators on device tensors ----------------------------------------------------------------
+namespace {
+
+// Makes `device` current and restores the caller's device at the end.
+struct DeviceScope {
+    int before = -1;
+    bool ok = false;
+    explicit DeviceScope(int device) {
+        if (cudaGetDevice(&before) != cudaSuccess) { before = -1; cudaGetLastError(); return; }
+        ok = before == device || cudaSetDevice(device) == cudaSuccess;
+        if (!ok) cudaGetLastError();
+    }
+    ~DeviceScope() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+};
+
+int sm_count(int device) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) { cudaGetLastError(); return 0; }
+    return n;
+}
+
+const char* kv4_shape_error(const kie_kv4_cache* c) {
+    if (!c) return "cache is NULL";
+    if (c->batch < 1 || c->n_kv_heads < 1 || c->max_ctx < 1) return "batch, n_kv_heads and max_ctx must be positive";
+    if (c->max_ctx > (1 << 30)) return "max_ctx above 2^30";
+    if (c->head_dim != 64 && c->head_dim != 128) return "head_dim must be 64 or 128";
+    if ((c->group != 32 && c->group != 64 && c->group != 128) || c->group > c->head_dim)
+        return "group must be 32, 64 or 128 and at most head_dim";
+    if (int64_t(c->batch) * c->n_kv_heads > (1 << 24)) return "batch * n_kv_heads above 2^24";
+    return nullptr;
+}
+
+// Byte offsets of the cache's parts: K codes, V codes, K params, V params.
+void kv4_offsets(const kie_kv4_cache* c, size_t* o) {
+    const size_t rows = size_t(c->batch) * c->n_kv_heads * kv4_pad(c->max_ctx);
+    const size_t codes = rows * (c->head_dim / 2), par = rows * (4 * (c->head_dim / c->group));
+    o[0] = 0; o[1] = codes; o[2] = 2 * codes; o[3] = 2 * codes + par; o[4] = 2 * codes + 2 * par;
+}
+
+Kv4 kv4_of(const kie_kv4_cache* c) {
+    size_t o[5];
+    kv4_offsets(c, o);
+    uint8_t* d = static_cast<uint8_t*>(c->data);
+    return Kv4{d + o[0], d + o[1], reinterpret_cast<uint16_t*>(d + o[2]), reinterpret_cast<uint16_t*>(d + o[3]),
+               c->batch, c->n_kv_heads, c->max_ctx, kv4_pad(c->max_ctx), c->head_dim, c->group};
+}
+
+Kv4Strides strides_of(const int64_t* s, int n, int heads, int dim) {
+    if (s) return Kv4Strides{s[0], s[1], s[2]};
+    return Kv4Strides{int64_t(n) * heads * dim, int64_t(heads) * dim, dim};
+}
+
+kie_status kv4_rows(const kie_kv4_cache* c, const void* k, const void* v, int32_t dtype, int32_t n_tokens,
+                    const int32_t* start) {
+    if (const char* why = kv4_shape_error(c)) return fail(nullptr, KIE_ERR_INVALID_ARG, "%s", why);
+    if (!c->data || (reinterpret_cast<uintptr_t>(c->data) & 255u)) return fail(nullptr, KIE_ERR_INVALID_ARG, "cache data is NULL or not 256-byte aligned");
+    if (dtype < 0 || dtype > 2) return fail(nullptr, KIE_ERR_INVALID_ARG, "bad dtype");
+    if (n_tokens < 0) return fail(nullptr, KIE_ERR_INVALID_ARG, "negative n_tokens");
+    const size_t mis = dtype == KIE_FP32 ? 3u : 1u;
+    if (n_tokens > 0 && (!k || !v || !start || (reinterpret_cast<uintptr_t>(k) & mis) || (reinterpret_cast<uintptr_t>(v) & mis) ||
+                         (reinterpret_cast<uintptr_t>(start) & 3u)))
+        return fail(nullptr, KIE_ERR_INVALID_ARG, "NULL or misaligned pointer");
+    // 256 threads hold 16 or 32 rows: the grid stays below 2^31 blocks
+    if (int64_t(c->batch) * c->n_kv_heads * n_tokens > (int64_t(1) << 34)) return fail(nullptr, KIE_ERR_UNSUPPORTED, "too many rows");
+    return KIE_OK;
+}
+
+const char* kv4_query_error(const kie_kv4_cache* c, const kie_kv4_query* q) {
+    if (const char* why = kv4_shape_error(c)) return why;
+    if (!q) return "query is NULL";
+    if (q->dtype < 0 || q->dtype > 2) return "bad dtype";
+    if (q->n_tokens < 0) return "negative n_tokens";
+    if (q->n_heads < 1 || q->n_heads % c->n_kv_heads) return "n_heads must be a positive multiple of n_kv_heads";
+    // 32-bit row indices inside a request, and one block per (8 rows, K/V head)
+    const int64_t rows = int64_t(q->n_tokens) * (q->n_heads / c->n_kv_heads);
+    if (rows > (1 << 30) || (rows + 7) / 8 * c->batch * c->n_kv_heads > (int64_t(1) << 30)) return "too many query rows";
+    return nullptr;
+}
+
+}  // namespace
+
+size_t kie_kv4_bytes(const kie_kv4_cache* c) {
+    if (kv4_shape_error(c)) return 0;
+    size_t o[5];
+    kv4_offsets(c, o);
+    return o[4];
+}
+
+kie_status kie_kv4_append(const kie_kv4_cache* c, const void* k, const void* v, int32_t dtype,
+                          const int64_t* k_strides, const int64_t* v_strides, int32_t n_tokens, const int32_t* start,
+                          const int32_t* n_tok, void* stream) {
+    const kie_status bad = kv4_rows(c, k, v, dtype, n_tokens, start);
+    if (bad != KIE_OK) return bad;
+    if (n_tokens == 0) return KIE_OK;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return fail(nullptr, KIE_ERR_CUDA, "cudaSetDevice(%d) failed", c->device);
+    const Kv4 kv = kv4_of(c);
+    const Kv4Strides ks = strides_of(k_strides, n_tokens, c->n_kv_heads, c->head_dim);
+    const Kv4Strides vs = strides_of(v_strides, n_tokens, c->n_kv_heads, c->head_dim);
+    KIE_CUDA(nullptr, kie_launch_kv4_append(&kv, k, v, &ks, &vs, dtype, n_tokens, start, n_tok, static_cast<cudaStream_t>(stream)));
+    return KIE_OK;
+}
+
+kie_status kie_kv4_read(const kie_kv4_cache* c, void* k, void* v, int32_t dtype, const int64_t* k_strides,
+                        const int64_t* v_strides, int32_t n_tokens, const int32_t* start, const int32_t* n_tok,
+                        void* stream) {
+    const kie_status bad = kv4_rows(c, k, v, dtype, n_tokens, start);
+    if (bad != KIE_OK) return bad;
+    if (n_tokens == 0) return KIE_OK;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return fail(nullptr, KIE_ERR_CUDA, "cudaSetDevice(%d) failed", c->device);
+    const Kv4 kv = kv4_of(c);
+    const Kv4Strides ks = strides_of(k_strides, n_tokens, c->n_kv_heads, c->head_dim);
+    const Kv4Strides vs = strides_of(v_strides, n_tokens, c->n_kv_heads, c->head_dim);
+    KIE_CUDA(nullptr, kie_launch_kv4_read(&kv, k, v, &ks, &vs, dtype, n_tokens, start, n_tok, static_cast<cudaStream_t>(stream)));
+    return KIE_OK;
+}
+
+size_t kie_kv4_attention_workspace(const kie_kv4_cache* c, const kie_kv4_query* q) {
+    if (kv4_query_error(c, q)) return 0;
+    const int sms = sm_count(c->device);
+    if (sms < 1) return 0;
+    const Kv4 kv = kv4_of(c);
+    return kie_kv4_attention_ws_floats(&kv, q->n_heads, q->n_tokens, q->dtype, sms) * 4;
+}
+
+kie_status kie_kv4_attention(const kie_kv4_cache* c, const kie_kv4_query* q, void* workspace, size_t ws_bytes,
+                             void* stream) {
+    if (const char* why = kv4_query_error(c, q)) return fail(nullptr, KIE_ERR_INVALID_ARG, "%s", why);
+    if (!c->data || (reinterpret_cast<uintptr_t>(c->data) & 255u)) return fail(nullptr, KIE_ERR_INVALID_ARG, "cache data is NULL or not 256-byte aligned");
+    if (q->causal != 0 && q->causal != 1) return fail(nullptr, KIE_ERR_INVALID_ARG, "causal must be 0 or 1");
+    if (q->window < 0 || (q->window > 0 && !q->causal)) return fail(nullptr, KIE_ERR_INVALID_ARG, "window must be 0, or positive with causal");
+    if (!std::isfinite(q->scale)) return fail(nullptr, KIE_ERR_INVALID_ARG, "scale is not finite");
+    if (q->n_tokens == 0) return KIE_OK;
+    const size_t mis = q->dtype == KIE_FP32 ? 3u : 1u;
+    if (!q->q || !q->out || !q->kv_len || (reinterpret_cast<uintptr_t>(q->q) & mis) || (reinterpret_cast<uintptr_t>(q->out) & mis) ||
+        (reinterpret_cast<uintptr_t>(q->kv_len) & 3u))
+        return fail(nullptr, KIE_ERR_INVALID_ARG, "NULL or misaligned pointer");
+    DeviceScope dev(c->device);
+    if (!dev.ok) return fail(nullptr, KIE_ERR_CUDA, "cudaSetDevice(%d) failed", c->device);
+    const int sms = sm_count(c->device);
+    if (sms < 1) return fail(nullptr, KIE_ERR_CUDA, "no multiprocessor count");
+    Kv4Attn a{};
+    a.c = kv4_of(c);
+    const size_t need = kie_kv4_attention_ws_floats(&a.c, q->n_heads, q->n_tokens, q->dtype, sms) * 4;
+    if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+        return fail(nullptr, KIE_ERR_OOM, "workspace too small or misaligned (need %zu bytes)", need);
+    a.q = q->q;
+    a.out = q->out;
+    a.qs = strides_of(q->q_strides, q->n_tokens, q->n_heads, c->head_dim);
+    a.os = strides_of(q->out_strides, q->n_tokens, q->n_heads, c->head_dim);
+    a.type = q->dtype;
+    a.heads = q->n_heads;
+    a.n_q = q->n_tokens;
+    a.kv_len = q->kv_len;
+    a.n_tok = q->n_tok;
+    a.causal = q->causal;
+    a.window = q->window;
+    a.scale = q->scale;
+    a.ws = static_cast<float*>(workspace);
+    KIE_CUDA(nullptr, kie_launch_kv4_attention(&a, sms, static_cast<cudaStream_t>(stream)));
+    return KIE_OK;
+}
+
+kie_status kie_sample(const kie_sample_args* a, void* stream) {
+    if (!a) return fail(nullptr, KIE_ERR_INVALID_ARG, "arguments are NULL");
+    if (a->dtype < 0 || a->dtype > 2) return fail(nullptr, KIE_ERR_INVALID_ARG, "bad dtype");
+    if (a->rows < 0 || a->vocab < 1) return fail(nullptr, KIE_ERR_INVALID_ARG, "negative rows or empty vocabulary");
+    if (a->vocab > KIE_SAMPLE_MAX_VOCAB) return fail(nullptr, KIE_ERR_UNSUPPORTED, "vocabulary above %d", KIE_SAMPLE_MAX_VOCAB);
+    if (a->rows > (1 << 24)) return fail(nullptr, KIE_ERR_UNSUPPORTED, "more than 2^24 rows");
+    if (a->rows == 0) return KIE_OK;
+    const size_t mis = a->dtype == KIE_FP32 ? 3u : 1u;
+    auto word = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (!a->logits || !a->u || !a->tokens || (reinterpret_cast<uintptr_t>(a->logits) & mis) || !word(a->u) || !word(a->tokens) ||
+        !word(a->probs) || !word(a->temperature) || !word(a->top_k) || !word(a->top_p) || !word(a->min_p))
+        return fail(nullptr, KIE_ERR_INVALID_ARG, "NULL or misaligned pointer");
+    DeviceScope dev(a->device);
+    if (!dev.ok) return fail(nullptr, KIE_ERR_CUDA, "cudaSetDevice(%d) failed", a->device);
+    const int sms = sm_count(a->device);
+    if (sms < 1) return fail(nullptr, KIE_ERR_CUDA, "no multiprocessor count");
+    SampleArgs s{a->logits, a->dtype, a->rows, a->vocab, a->row_stride, a->temperature, a->top_k, a->top_p, a->min_p,
+                 a->u, a->tokens, a->probs, nullptr};
+    KIE_CUDA(nullptr, kie_launch_sample(&s, sms, static_cast<cudaStream_t>(stream)));
     return KIE_OK;
 }
 

@@ -1,0 +1,553 @@
+// A token per row of logits by temperature, top-k, top-p and min-p from given
+// random numbers.
+//
+// With m the row's largest logit and w_i = exp((l_i - m) / T), the tokens kept
+// are a prefix of the order (logit descending, index ascending), cut by top-k
+// (length), top-p (the shortest prefix with p of the top-k prefix's mass) and
+// min-p (w_i >= min_p); the drawn token is the first, in index order, at which
+// the running mass of the kept tokens passes u times their total.
+//
+// Tokens are whole numbers, so the masses that decide them must not depend on
+// the order of a sum: w_i is computed to about 2^-43 in pairs of fp32 numbers
+// (fp64 runs at 1/64 of their rate here) and kept as an integer count of
+// 2^-44.  Sums of integers are exact in any order, so the threads, the shared-
+// memory atomics and the CTAs of a cluster give one answer, and a token differs
+// from the definition's only where u falls within about 2^-37 of a border.
+//
+// One cluster per row, the row's logits read once into its CTAs' shared memory.
+// The prefix's end is found by a histogram over y = (m - l) log2(e) / T in steps
+// of 1/16 (counts and masses), a second one inside the bin that holds the end,
+// and then among the few tokens left (or, for crowds of near-equal logits, by
+// further histograms over the bits of the logit).  No sort.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "kie_device.cuh"
+#include "kie_sample.h"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int NT = 512, NWARP = NT / 32;   // threads per CTA
+constexpr int NB = 1024;                   // histogram bins (two per thread)
+constexpr int FRAC = 44;                   // masses count 2^-44
+constexpr int LIST = 32;                   // candidates resolved by one warp
+constexpr int MAXC = 8;                    // CTAs per row
+
+// 2^(-j/128) * 2^63, by the series of exp(-j ln 2 / 128) (to 2^-52)
+struct Pow2 { uint64_t v[128]; };
+constexpr Pow2 make_pow2() {
+    Pow2 t{};
+    for (int j = 0; j < 128; ++j) {
+        const double a = -0.693147180559945309417 * j / 128.0;
+        double s = 0.0;
+        for (int k = 24; k >= 1; --k) s = (1.0 + s) * a / k;   // a + a^2/2! + ...
+        t.v[j] = uint64_t((1.0 + s) * 9223372036854775808.0);
+    }
+    return t;
+}
+__device__ constexpr Pow2 kPow2 = make_pow2();
+
+struct Shared {
+    uint32_t h[4][NB];          // local histogram: counts, three 15-bit limbs of the masses
+    uint32_t fc[2][NB];         // this CTA's share of the summed histogram: counts, masses
+    uint64_t fm[2][NB];
+    uint64_t table[128];        // 2^(-j/128) * 2^63
+    uint64_t xch[4][4];         // values other CTAs read, by exchange number
+    uint64_t list_w[LIST];
+    uint32_t list_key[LIST];
+    int32_t list_idx[LIST];
+    uint32_t list_n;
+    uint64_t wsum[NWARP];
+    uint32_t wcnt[NWARP];
+    uint32_t wmin[NWARP], wmax[NWARP];
+    // result of find()
+    int32_t f_bin;
+    uint32_t f_cnt, f_n;
+    uint64_t f_mass, f_m;
+    // result of select()
+    uint32_t key, n_eq, all_eq;
+    uint64_t mass;
+    float chi, clo;
+    int32_t token;
+    uint64_t token_w;
+};
+
+template <int T> __device__ __forceinline__ float to_float(const void* p, int64_t i);
+template <> __device__ __forceinline__ float to_float<0>(const void* p, int64_t i) { return __half2float(static_cast<const __half*>(p)[i]); }
+template <> __device__ __forceinline__ float to_float<1>(const void* p, int64_t i) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]); }
+template <> __device__ __forceinline__ float to_float<2>(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+
+// Order-preserving integer of a float (-0 and 0 are one value).
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// What weights need of a row: its maximum and log2(e)/T as a sum of two floats.
+struct Row {
+    float m, chi, clo;
+    const uint64_t* table;
+    // (m - l) log2(e) / T in fp32: monotone in l
+    __device__ __forceinline__ float y(float l) const { return (m - l) * chi; }
+    // exp((l - m) / T) in units of 2^-44, to about 2^-43 relative
+    __device__ __forceinline__ uint64_t weight(float l) const {
+        const float hi = m - l;
+        const float yh = hi * chi;
+        if (!(yh < 46.f)) return 0;                        // below half a unit (l = -inf too)
+        const float bb = hi - m, lo = (m - (hi - bb)) - (l + bb);   // m - l = hi + lo exactly
+        const float yl = fmaf(hi, clo, fmaf(lo, chi, fmaf(hi, chi, -yh)));
+        // y = k / 128 + f + yl, |f| <= 1/256, f exact
+        const float kf = rintf(yh * 128.f);
+        const float f = fmaf(kf, -1.f / 128.f, yh);
+        const int k = int(kf);
+        // 2^-(f + yl) = 1 - a + a^2/2 - ..., a = (f + yl) ln 2 = ah + al
+        constexpr float L1 = 0.693147182464599609375f, L2 = -1.904654299957767e-9f;   // ln 2 = L1 + L2
+        const float ah = f * L1;
+        const float al = fmaf(yl, L1, fmaf(f, L2, fmaf(f, L1, -ah)));
+        const float q = fmaf(ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al * fmaf(al, 0.5f, ah));
+        // to units of 2^-48: the large term in two exact steps, the small ones (below 2^-17) in one
+        const float a1 = rintf(ah * 1048576.f);                     // 2^20
+        const float a2 = fmaf(ah, 1048576.f, -a1) * 268435456.f;    // the rest, 2^48
+        const int64_t F = (int64_t(1) << 48) - (int64_t(int(a1)) << 28) - int64_t(__float2int_rn(a2)) +
+                          int64_t(__float2int_rn((q - al) * 70368744177664.f)) * 4;
+        const uint64_t p = __umul64hi(uint64_t(F) << 14, table[k & 127]);   // 2^(62 + 63 - 64) = 2^61
+        const int sh = 61 - FRAC + (k >> 7);
+        return sh >= 64 ? 0 : (p + (uint64_t(1) << (sh - 1))) >> sh;
+    }
+};
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ int bin_of(float y) { return y < float(NB - 1) / 16.f ? int(y * 16.f) : NB - 1; }
+__device__ __forceinline__ int sub_of(float y, int b) {
+    const float f = (fminf(y, 1.0e9f) * 16.f - float(b)) * float(NB);
+    return f < float(NB - 1) ? int(f) : NB - 1;
+}
+
+template <int T>
+__global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const int S) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
+    float* x = reinterpret_cast<float*>(smem_raw + (sizeof(Shared) + 15) / 16 * 16);
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    const int row = int(blockIdx.x) / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int s0 = min(rank * S, A.vocab), n = min(S, A.vocab - s0);
+    int ex = 0;   // exchange number: its values stay put for three more exchanges
+    auto sync = [&]() { if (C > 1) cl.sync(); else __syncthreads(); };
+
+    // ---- read the slice, its maximum
+    float mx = -INFINITY;
+    {
+        const int64_t base = int64_t(row) * A.row_stride + s0;
+        for (int i = tid; i < n; i += NT) {
+            float v = to_float<T>(A.logits, base + i);
+            if (v != v) v = -INFINITY;
+            x[i] = v;
+            mx = fmaxf(mx, v);
+        }
+        if (tid < 128) sh.table[tid] = kPow2.v[tid];
+        if (tid == 0) {
+            const float t = A.temperature ? A.temperature[row] : 1.f;
+            const double c = fmin(1.4426950408889634074 / double(t), 3.0e38);
+            sh.chi = float(c);
+            sh.clo = float(c - double(float(c)));
+        }
+    }
+    mx = kie::warp_max(mx);
+    if (lane == 0) sh.wmax[warp] = __float_as_uint(mx);
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < NWARP; ++w) mx = fmaxf(mx, __uint_as_float(sh.wmax[w]));
+        sh.xch[ex][0] = __float_as_uint(mx);
+    }
+    sync();
+    mx = -INFINITY;
+    for (int r = 0; r < C; ++r) mx = fmaxf(mx, __uint_as_float(uint32_t(cl.map_shared_rank(&sh, r)->xch[ex][0])));
+    ex = (ex + 1) & 3;
+
+    const float temp = A.temperature ? A.temperature[row] : 1.f;
+    if (mx == -INFINITY) {               // nothing to choose from
+        if (rank == 0 && tid == 0) {
+            A.tokens[row] = -1;
+            if (A.tokens2) A.tokens2[row] = -1;
+            if (A.probs) A.probs[row] = 0.f;
+        }
+        sync();
+        return;
+    }
+    if (!(temp > 0.f)) {                 // greedy: the lowest index of the largest logit
+        uint32_t at = 0xFFFFFFFFu;
+        for (int i = tid; i < n; i += NT) if (x[i] == mx) { at = uint32_t(s0 + i); break; }
+        at = __reduce_min_sync(0xffffffffu, at);
+        __syncthreads();
+        if (lane == 0) sh.wmin[warp] = at;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 1; w < NWARP; ++w) at = min(at, sh.wmin[w]);
+            sh.xch[ex][0] = at;
+        }
+        sync();
+        if (rank == 0 && tid == 0) {
+            for (int r = 1; r < C; ++r) at = min(at, uint32_t(cl.map_shared_rank(&sh, r)->xch[ex][0]));
+            A.tokens[row] = int32_t(at);
+            if (A.tokens2) A.tokens2[row] = int32_t(at);
+            if (A.probs) A.probs[row] = 1.f;
+        }
+        sync();
+        return;
+    }
+    if (mx == INFINITY) {                // infinite logits share the mass
+        for (int i = tid; i < n; i += NT) x[i] = x[i] == INFINITY ? 0.f : -INFINITY;
+        mx = 0.f;
+        __syncthreads();
+    }
+    const Row R{mx, sh.chi, sh.clo, sh.table};
+
+    const int top_k = A.top_k ? A.top_k[row] : 0;
+    const float top_p = A.top_p ? A.top_p[row] : 1.f;
+    const bool use_k = top_k > 0 && top_k < A.vocab, use_p = top_p < 1.f;
+
+    // Histogram of the elements for which binf gives a bin (>= 0), summed over the
+    // cluster: afterwards each CTA holds its share of the sums in fc/fm[which].
+    auto histogram = [&](int which, auto binf) {
+        for (int i = tid; i < 4 * NB; i += NT) (&sh.h[0][0])[i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < n; i += NT) {
+            const float l = x[i];
+            const int b = binf(l);
+            if (b >= 0) {
+                atomicAdd(&sh.h[0][b], 1u);
+                const uint64_t w = R.weight(l);
+                if (w) {
+                    atomicAdd(&sh.h[1][b], uint32_t(w) & 0x7FFFu);
+                    atomicAdd(&sh.h[2][b], uint32_t(w >> 15) & 0x7FFFu);
+                    atomicAdd(&sh.h[3][b], uint32_t(w >> 30));
+                }
+            }
+        }
+        sync();
+        const int per = NB / C;
+        for (int i = tid; i < per; i += NT) {
+            const int b = rank * per + i;
+            uint32_t cnt = 0;
+            uint64_t ms = 0;
+            for (int r = 0; r < C; ++r) {
+                const Shared* o = cl.map_shared_rank(&sh, r);
+                cnt += o->h[0][b];
+                ms += uint64_t(o->h[1][b]) + (uint64_t(o->h[2][b]) << 15) + (uint64_t(o->h[3][b]) << 30);
+            }
+            sh.fc[which][b] = cnt;
+            sh.fm[which][b] = ms;
+        }
+        sync();
+    };
+    // The bin of a summed histogram in which the running count (by_mass: mass)
+    // reaches `target`; what precedes it and what it holds go to sh.f_*.
+    auto find = [&](int which, bool by_mass, uint64_t target, uint32_t cnt0, uint64_t mass0) {
+        const Shared* o = cl.map_shared_rank(&sh, (2 * tid) / (NB / C));
+        const uint32_t c0 = o->fc[which][2 * tid], c1 = o->fc[which][2 * tid + 1];
+        const uint64_t m0 = o->fm[which][2 * tid], m1 = o->fm[which][2 * tid + 1];
+        uint32_t ci = c0 + c1;
+        uint64_t mi = m0 + m1;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t cy = __shfl_up_sync(0xffffffffu, ci, d);
+            const uint64_t my = __shfl_up_sync(0xffffffffu, mi, d);
+            if (lane >= d) { ci += cy; mi += my; }
+        }
+        __syncthreads();                 // the last find's results and sums have been read
+        if (lane == 31) { sh.wcnt[warp] = ci; sh.wsum[warp] = mi; }
+        __syncthreads();
+        uint32_t cb = cnt0 + ci - (c0 + c1);
+        uint64_t mb = mass0 + mi - (m0 + m1);
+        for (int w = 0; w < warp; ++w) { cb += sh.wcnt[w]; mb += sh.wsum[w]; }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t cj = j ? c1 : c0;
+            const uint64_t mj = j ? m1 : m0;
+            const uint64_t before = by_mass ? mb : cb, with = by_mass ? mb + mj : uint64_t(cb) + cj;
+            if (before < target && target <= with) {
+                sh.f_bin = 2 * tid + j;
+                sh.f_cnt = cb;
+                sh.f_mass = mb;
+                sh.f_n = cj;
+                sh.f_m = mj;
+            }
+            cb += cj;
+            mb += mj;
+        }
+        __syncthreads();
+    };
+    // The shortest prefix whose count (mass) reaches target: it ends with the
+    // n_eq lowest-indexed of the all_eq tokens of logit of_key(key).
+    auto select = [&](bool by_mass, uint64_t target) {
+        find(0, by_mass, target, 0u, 0ull);
+        const int b = sh.f_bin;
+        uint32_t cnt = sh.f_cnt;
+        uint64_t mass = sh.f_mass;
+        histogram(1, [&](float l) { const float y = R.y(l); return bin_of(y) == b ? sub_of(y, b) : -1; });
+        find(1, by_mass, target, cnt, mass);
+        const int s = sh.f_bin;
+        cnt = sh.f_cnt;
+        mass = sh.f_mass;
+        const uint32_t nc = sh.f_n;
+        auto here = [&](float l) { const float y = R.y(l); return bin_of(y) == b && sub_of(y, b) == s; };
+        if (nc <= LIST) {
+            if (tid == 0) sh.list_n = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += NT)
+                if (here(x[i])) {
+                    const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                    sh.list_key[at] = key_of(x[i]);
+                    sh.list_idx[at] = s0 + i;
+                    sh.list_w[at] = R.weight(x[i]);
+                }
+            sync();
+            if (warp == 0) {
+                uint32_t key = 0u;
+                int32_t idx = 0x7FFFFFFF;
+                uint64_t w = 0;
+                int k = lane;
+                for (int r = 0; r < C; ++r) {
+                    const Shared* o = cl.map_shared_rank(&sh, r);
+                    const int m = int(o->list_n);
+                    if (k >= 0 && k < m) { key = o->list_key[k]; idx = o->list_idx[k]; w = o->list_w[k]; k = -1; }
+                    else if (k >= 0) k -= m;
+                }
+                const bool have = idx != 0x7FFFFFFF;
+                uint32_t before = 0, eq = 0, eq_all = 0;
+                uint64_t mb = 0;
+                for (int j = 0; j < 32; ++j) {
+                    const uint32_t kj = __shfl_sync(0xffffffffu, key, j);
+                    const int32_t ij = __shfl_sync(0xffffffffu, idx, j);
+                    const uint64_t wj = __shfl_sync(0xffffffffu, w, j);
+                    if (ij == 0x7FFFFFFF) continue;
+                    if (kj > key || (kj == key && ij < idx)) { ++before; mb += wj; }
+                    if (kj == key) { ++eq_all; if (ij <= idx) ++eq; }
+                }
+                const uint64_t with = by_mass ? mass + mb + w : uint64_t(cnt) + before + 1;
+                const uint64_t without = by_mass ? mass + mb : uint64_t(cnt) + before;
+                // equal masses before and after (w = 0) cannot both straddle the target
+                if (have && without < target && target <= with) {
+                    sh.key = key;
+                    sh.n_eq = eq;
+                    sh.all_eq = eq_all;
+                    sh.mass = mass + mb + w;
+                }
+            }
+            sync();                      // the lists may be written again
+            return;
+        }
+        // many near-equal logits: their keys' range, then its bits
+        uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+        for (int i = tid; i < n; i += NT)
+            if (here(x[i])) { const uint32_t k = key_of(x[i]); lo = min(lo, k); hi = max(hi, k); }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) { sh.wmin[warp] = lo; sh.wmax[warp] = hi; }
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 1; w < NWARP; ++w) { lo = min(lo, sh.wmin[w]); hi = max(hi, sh.wmax[w]); }
+            sh.xch[ex][0] = uint64_t(hi) << 32 | lo;
+        }
+        sync();
+        lo = 0xFFFFFFFFu;
+        hi = 0u;
+        for (int r = 0; r < C; ++r) {
+            const uint64_t v = cl.map_shared_rank(&sh, r)->xch[ex][0];
+            lo = min(lo, uint32_t(v));
+            hi = max(hi, uint32_t(v >> 32));
+        }
+        ex = (ex + 1) & 3;
+        for (int level = 0; level < 5; ++level) {   // 2^32 -> 2^22 -> 2^12 -> 2^2 -> 1 keys
+            int shift = 0;
+            while (shift < 22 && ((hi - lo) >> shift) >= NB) ++shift;
+            histogram(1, [&](float l) { const uint32_t k = key_of(l); return k >= lo && k <= hi ? int((hi - k) >> shift) : -1; });
+            find(1, by_mass, target, cnt, mass);
+            cnt = sh.f_cnt;
+            mass = sh.f_mass;
+            hi -= uint32_t(sh.f_bin) << shift;
+            if (shift == 0) {
+                if (tid == 0) {
+                    const uint64_t w = R.weight(of_key(hi));
+                    const uint32_t all = sh.f_n;
+                    const uint64_t need = by_mass ? (w ? (target - mass + w - 1) / w : all) : target - cnt;
+                    sh.key = hi;
+                    sh.all_eq = all;
+                    sh.n_eq = uint32_t(need < all ? need : all);
+                    sh.mass = mass + sh.n_eq * w;
+                }
+                __syncthreads();
+                return;
+            }
+            lo = max(lo, hi - ((1u << shift) - 1u));
+        }
+    };
+
+    // ---- the kept prefix: every logit above `key`, and the n_eq lowest-indexed equal to it
+    uint32_t key = 0u, n_eq = 0xFFFFFFFFu, all_eq = 0u;
+    if (use_k || use_p) {
+        histogram(0, [&](float l) { return bin_of(R.y(l)); });
+        uint64_t mass = 0;
+        if (use_k) {
+            select(false, uint64_t(top_k));
+            __syncthreads();
+            mass = sh.mass;
+            key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
+        } else {
+            // all of it
+            find(0, false, uint64_t(A.vocab), 0u, 0ull);
+            mass = sh.f_mass + sh.f_m;
+        }
+        if (use_p) {
+            // ceil(p * mass), at least one token
+            const uint64_t P = top_p > 0.f ? uint64_t(double(top_p) * 18446744073709551616.0) : 0ull;
+            uint64_t target = __umul64hi(mass, P) + (mass * P != 0ull ? 1ull : 0ull);
+            if (target == 0) target = 1;
+            select(true, target);
+            __syncthreads();
+            key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
+        }
+    }
+    const float min_p = A.min_p ? A.min_p[row] : 0.f;
+    const uint64_t wmin = min_p > 0.f ? uint64_t(ceil(double(fminf(min_p, 1.f)) * double(1ull << FRAC))) : 0ull;
+
+    // ---- masses in index order: warp `warp` holds elements [i0, i1) of the slice
+    const int per = (n + NWARP * 32 - 1) / (NWARP * 32) * 32;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+    uint32_t eq0 = 0;                    // equal tokens before this warp's
+    const bool ties = n_eq < all_eq;
+    if (ties) {
+        uint32_t c = 0;
+        for (int i = i0 + lane; i < i1; i += 32) c += key_of(x[i]) == key;
+        c = __reduce_add_sync(0xffffffffu, c);
+        __syncthreads();
+        if (lane == 0) sh.wcnt[warp] = c;
+        __syncthreads();
+        if (tid == 0) {
+            uint64_t a = 0;
+            for (int w = 0; w < NWARP; ++w) a += sh.wcnt[w];
+            sh.xch[ex][1] = a;
+        }
+        sync();
+        for (int r = 0; r < rank; ++r) eq0 += uint32_t(cl.map_shared_rank(&sh, r)->xch[ex][1]);
+        for (int w = 0; w < warp; ++w) eq0 += sh.wcnt[w];
+        ex = (ex + 1) & 3;
+    }
+    // kept mass of element i (lanes in index order); eq: equal tokens before this group of 32
+    auto kept = [&](int i, uint32_t& eq) -> uint64_t {
+        const float l = i < i1 ? x[i] : -INFINITY;
+        const uint32_t k = key_of(l);
+        bool keep = i < i1 && k >= key;
+        if (ties) {
+            const uint32_t same = __ballot_sync(0xffffffffu, i < i1 && k == key);
+            if (k == key) keep = keep && eq + __popc(same & ((1u << lane) - 1u)) < n_eq;
+            eq += __popc(same);
+        }
+        if (!keep) return 0;
+        const uint64_t w = R.weight(l);
+        return w >= wmin ? w : 0;
+    };
+    uint64_t sum = 0;
+    {
+        uint32_t eq = eq0;
+        for (int i = i0; i < i1; i += 32) sum += kept(i + lane, eq);
+    }
+    sum = warp_sum64(sum);
+    __syncthreads();
+    if (lane == 0) sh.wsum[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+        uint64_t a = 0;
+        for (int w = 0; w < NWARP; ++w) a += sh.wsum[w];
+        sh.xch[ex][2] = a;
+    }
+    sync();
+    uint64_t total = 0, start = 0;
+    for (int r = 0; r < C; ++r) {
+        const uint64_t v = cl.map_shared_rank(&sh, r)->xch[ex][2];
+        if (r < rank) start += v;
+        total += v;
+    }
+    for (int w = 0; w < warp; ++w) start += sh.wsum[w];
+    const float uf = A.u[row];
+    const uint64_t U = uf >= 1.f ? ~0ull : uf > 0.f ? uint64_t(double(uf) * 18446744073709551616.0) : 0ull;
+    const uint64_t target = __umul64hi(total, U);
+    if (start <= target && target < start + sum) {       // this warp holds the crossing
+        uint32_t eq = eq0;
+        for (int i = i0; i < i1; i += 32) {
+            const uint64_t w = kept(i + lane, eq);
+            uint64_t inc = w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += v;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, start + inc > target);
+            if (hit) {
+                if (lane == __ffs(hit) - 1) {
+                    A.tokens[row] = s0 + i + lane;
+                    if (A.tokens2) A.tokens2[row] = s0 + i + lane;
+                    if (A.probs) A.probs[row] = float(double(w) / double(total));
+                }
+                break;
+            }
+            start += __shfl_sync(0xffffffffu, inc, 31);
+        }
+    }
+    sync();                              // no CTA leaves while another may read its shared memory
+}
+
+template <int T>
+cudaError_t launch(const SampleArgs& a, int C, int S, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const int smem = int((sizeof(Shared) + 15) / 16 * 16) + S * 4;
+    int dev = 0;
+    cudaError_t r = cudaGetDevice(&dev);
+    if (r != cudaSuccess) return r;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev >= 64 || !(done.load(std::memory_order_acquire) & bit)) {
+        r = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        if (r != cudaSuccess) return r;
+        if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(a.rows) * C);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, S);
+}
+
+}  // namespace
+
+extern "C" cudaError_t kie_launch_sample(const SampleArgs* a, int sms, cudaStream_t st) {
+    // CTAs per row: enough to fill the GPU with few rows, and at least so many
+    // that a slice fits shared memory
+    int C = 1;
+    while (C < MAXC && (int64_t(a->rows) * C < sms || int64_t(a->vocab) > int64_t(C) * 32768) && a->vocab > C * 1024) C *= 2;
+    const int S = ((a->vocab + C - 1) / C + 7) / 8 * 8;
+    if (a->type == 0) return launch<0>(*a, C, S, st);
+    if (a->type == 1) return launch<1>(*a, C, S, st);
+    return launch<2>(*a, C, S, st);
+}

@@ -56,6 +56,24 @@ class kie_weights(C.Structure):
                 ("layers", C.POINTER(kie_layer_weights)), ("on_device", C.c_int32)]
 
 
+class kie_kv4_cache(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("batch", C.c_int32), ("n_kv_heads", C.c_int32), ("max_ctx", C.c_int32),
+                ("head_dim", C.c_int32), ("group", C.c_int32), ("device", C.c_int32)]
+
+
+class kie_kv4_query(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("out", C.c_void_p), ("q_strides", C.c_void_p), ("out_strides", C.c_void_p),
+                ("kv_len", C.c_void_p), ("n_tok", C.c_void_p), ("dtype", C.c_int32), ("n_tokens", C.c_int32),
+                ("n_heads", C.c_int32), ("causal", C.c_int32), ("window", C.c_int32), ("scale", C.c_float)]
+
+
+class kie_sample_args(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("dtype", C.c_int32), ("rows", C.c_int32), ("vocab", C.c_int32),
+                ("row_stride", C.c_int64), ("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p),
+                ("min_p", C.c_void_p), ("u", C.c_void_p), ("tokens", C.c_void_p), ("probs", C.c_void_p),
+                ("device", C.c_int32)]
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "kie_workspace_bytes": (C.c_size_t, [C.POINTER(kie_config)]),
@@ -89,6 +107,15 @@ EXPORTS = {
     "kie_quantize_fp8_rows": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p]),
     "kie_quantize_nvfp4_rows": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
     "kie_convert_fp8_e5m2": (C.c_int, [C.c_void_p, C.c_size_t, C.c_void_p]),
+    "kie_kv4_bytes": (C.c_size_t, [C.POINTER(kie_kv4_cache)]),
+    "kie_kv4_append": (C.c_int, [C.POINTER(kie_kv4_cache), C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                 C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "kie_kv4_read": (C.c_int, [C.POINTER(kie_kv4_cache), C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                               C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "kie_kv4_attention_workspace": (C.c_size_t, [C.POINTER(kie_kv4_cache), C.POINTER(kie_kv4_query)]),
+    "kie_kv4_attention": (C.c_int, [C.POINTER(kie_kv4_cache), C.POINTER(kie_kv4_query), C.c_void_p, C.c_size_t,
+                                    C.c_void_p]),
+    "kie_sample": (C.c_int, [C.POINTER(kie_sample_args), C.c_void_p]),
 }
 
 _lib = None
@@ -349,3 +376,170 @@ def convert_fp8_e5m2(x16: np.ndarray) -> np.ndarray:
     out = np.empty(x.size, np.uint8)
     _check(load().kie_convert_fp8_e5m2(_ptr(x), x.size, _ptr(out)))
     return out
+
+
+# ---- operators on device tensors ---------------------------------------------------------------
+# torch CUDA tensors in and out, enqueued on torch's current stream of their
+# device (or on `stream`, a torch.cuda.Stream).  Results are allocated by torch
+# where `out` is not given.
+DTYPES = {"float16": 0, "bfloat16": 1, "float32": 2}
+
+
+def _dtype(t):
+    name = str(t.dtype).replace("torch.", "")
+    if name not in DTYPES:
+        raise ValueError(f"tensors must be float16, bfloat16 or float32, not {name}")
+    return DTYPES[name]
+
+
+def _on(t, device, what):
+    if not getattr(t, "is_cuda", False) or t.device.index != device:
+        raise ValueError(f"{what} must be a CUDA tensor on device {device}")
+
+
+def _vector(t, n, dtype, device, what):
+    """Address of a contiguous [n] tensor of `dtype` ("int32", "float32"); None stays None."""
+    if t is None:
+        return None
+    _on(t, device, what)
+    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape ({n},)")
+    return t.data_ptr()
+
+
+def _rows(t, shape, device, what):
+    """(address, strides) of a 4-D tensor whose channels are contiguous."""
+    _on(t, device, what)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{what} must have contiguous channels")
+    return t.data_ptr(), (C.c_int64 * 3)(*t.stride()[:3])
+
+
+def _written(t, what):
+    """A tensor that a kernel writes must not hold one element twice."""
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{what} must not be broadcast")
+
+
+def _stream(stream, device):
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+class KV4Cache:
+    """A 4-bit K/V cache of one layer (kie_kv4_cache): `batch` requests of up to
+    max_ctx positions, n_kv_heads heads of head_dim 64 or 128, a scale and a zero
+    per `group` channels.  Its memory is a torch tensor (`data`)."""
+
+    def __init__(self, batch: int, n_kv_heads: int, max_ctx: int, head_dim: int, group: int = 32, device=None):
+        import torch
+        device = torch.device("cuda" if device is None else device)
+        index = torch.cuda.current_device() if device.index is None else device.index
+        self.desc = kie_kv4_cache(None, batch, n_kv_heads, max_ctx, head_dim, group, index)
+        n = load().kie_kv4_bytes(C.byref(self.desc))
+        if n == 0:
+            raise ValueError(f"no 4-bit cache of shape batch {batch}, heads {n_kv_heads}, max_ctx {max_ctx}, "
+                             f"head_dim {head_dim}, group {group}")
+        self.data = torch.empty(n, dtype=torch.uint8, device=f"cuda:{index}")
+        self.desc.data = self.data.data_ptr()
+
+    @property
+    def device(self) -> int:
+        return self.desc.device
+
+    def _shape(self, n):
+        return self.desc.batch, n, self.desc.n_kv_heads, self.desc.head_dim
+
+    def append(self, k, v, start, n_tok=None, stream=None):
+        """kie_kv4_append: store k, v [batch, tokens, n_kv_heads, head_dim] (any
+        strides with contiguous channels) at positions start[b] + t, t < n_tok[b]."""
+        d = self.desc
+        if k.dim() != 4 or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-D tensors of one type")
+        n = k.shape[1]
+        kp, ks = _rows(k, self._shape(n), d.device, "k")
+        vp, vs = _rows(v, self._shape(n), d.device, "v")
+        _check(load().kie_kv4_append(C.byref(d), kp, vp, _dtype(k), ks, vs, n,
+                                     _vector(start, d.batch, "int32", d.device, "start"),
+                                     _vector(n_tok, d.batch, "int32", d.device, "n_tok"), _stream(stream, d.device)))
+
+    def read(self, start, tokens: int, n_tok=None, out=None, dtype=None, stream=None):
+        """kie_kv4_read: the values at positions start[b] + t, t < n_tok[b], as
+        (k, v) [batch, tokens, n_kv_heads, head_dim]: `out`, or new tensors of
+        `dtype` (float16) with zeros in the rows that are not read."""
+        import torch
+        d = self.desc
+        if out is None:
+            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(d.device):
+                out = [torch.zeros(self._shape(tokens), dtype=dtype or torch.float16, device=self.data.device)
+                       for _ in range(2)]
+        k, v = out
+        if k.dtype != v.dtype:
+            raise ValueError("the two outputs must be of one type")
+        kp, ks = _rows(k, self._shape(tokens), d.device, "out[0]")
+        vp, vs = _rows(v, self._shape(tokens), d.device, "out[1]")
+        _written(k, "out[0]")
+        _written(v, "out[1]")
+        _check(load().kie_kv4_read(C.byref(d), kp, vp, _dtype(k), ks, vs, tokens,
+                                   _vector(start, d.batch, "int32", d.device, "start"),
+                                   _vector(n_tok, d.batch, "int32", d.device, "n_tok"), _stream(stream, d.device)))
+        return k, v
+
+    def attention(self, q, kv_len, n_tok=None, causal=True, window: int = 0, scale=None, out=None, stream=None):
+        """kie_kv4_attention of q [batch, tokens, n_heads, head_dim] over the
+        stored positions: `out`, or a new tensor like q with zeros in the rows
+        from n_tok[b] on.  scale: 1/sqrt(head_dim) unless given."""
+        import torch
+        d = self.desc
+        if q.dim() != 4:
+            raise ValueError("q must be a 4-D tensor")
+        n, heads = q.shape[1], q.shape[2]
+        shape = (d.batch, n, heads, d.head_dim)
+        qp, qs = _rows(q, shape, d.device, "q")
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(d.device):
+            if out is None:
+                out = (torch.empty if n_tok is None else torch.zeros)(shape, dtype=q.dtype, device=q.device)
+            elif out.dtype != q.dtype:
+                raise ValueError("out must have q's type")
+            op, os_ = _rows(out, shape, d.device, "out")
+            _written(out, "out")
+            a = kie_kv4_query(qp, op, C.cast(qs, C.c_void_p), C.cast(os_, C.c_void_p),
+                              _vector(kv_len, d.batch, "int32", d.device, "kv_len"),
+                              _vector(n_tok, d.batch, "int32", d.device, "n_tok"), _dtype(q), n, heads,
+                              int(bool(causal)), int(window),
+                              float(d.head_dim ** -0.5 if scale is None else scale))
+            ws_bytes = load().kie_kv4_attention_workspace(C.byref(d), C.byref(a))
+            # of the stream that the kernels run on: the allocator gives it to no
+            # one else before they are done, and a graph keeps its own
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            _check(load().kie_kv4_attention(C.byref(d), C.byref(a), ws.data_ptr(), ws_bytes,
+                                            _stream(stream, d.device)))
+        return out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+    """kie_sample: a token per row of logits [rows, vocab] (contiguous within a
+    row) from the random numbers u [rows], and its probability: (int32 [rows],
+    fp32 [rows]), written to `tokens` and `probs` where given."""
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D CUDA tensor")
+    if logits.shape[1] > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must be contiguous within a row")
+    rows, vocab = logits.shape
+    dev = logits.device.index
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+        if tokens is None:
+            tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        if probs is None:
+            probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        a = kie_sample_args(logits.data_ptr(), _dtype(logits), rows, vocab, logits.stride(0),
+                            _vector(temperature, rows, "float32", dev, "temperature"),
+                            _vector(top_k, rows, "int32", dev, "top_k"), _vector(top_p, rows, "float32", dev, "top_p"),
+                            _vector(min_p, rows, "float32", dev, "min_p"), _vector(u, rows, "float32", dev, "u"),
+                            _vector(tokens, rows, "int32", dev, "tokens"), _vector(probs, rows, "float32", dev, "probs"),
+                            dev)
+        _check(load().kie_sample(C.byref(a), _stream(stream, dev)))
+    return tokens, probs

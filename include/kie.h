@@ -360,6 +360,131 @@ kie_status kie_quantize_nvfp4_rows(const uint16_t* w_fp16, int32_t rows, int32_t
  * conversion; xAI page sections 2.3 and 4.3).  NaN stays NaN. */
 kie_status kie_convert_fp8_e5m2(const uint16_t* x_fp16, size_t n, uint8_t* out);
 
+/* ---- operators on device tensors --------------------------------------------------------------
+ * Stateless calls on device memory, enqueued on `stream` (a cudaStream_t; NULL:
+ * the legacy default stream) of the device they name, without synchronising.
+ * They allocate nothing and keep no pointer, so they may be captured into CUDA
+ * graphs; calls on different streams are independent as long as their buffers
+ * are.  Arguments that the host can see are checked before anything is
+ * launched; values in device memory (lengths, positions, ids) are clamped to
+ * their buffers as each call says.  The calling thread's current device is
+ * restored.  kie_last_error(NULL) has the message of a failure.
+ *
+ * Element types of their tensors. */
+typedef enum { KIE_FP16 = 0, KIE_BF16 = 1, KIE_FP32 = 2 } kie_dtype;
+
+/* A K/V cache in 4 bits, one layer of `batch` requests.  Each group of `group`
+ * channels of one position and head keeps, of its values rounded to fp16
+ * (nearest even, saturating at +-65504; a NaN is stored as 0: the format has
+ * none), z = their minimum and s = fp16((maximum - minimum) / 15) and, per
+ * value, code = clamp(round_half_even((x - z) / s), 0, 15) (fp32 IEEE
+ * difference and quotient; 0 where s is 0).  It stands for code * s + z.
+ * data: device memory of kie_kv4_bytes() bytes, 256-byte aligned, the caller's;
+ * its contents need no initialisation (positions never stored must lie at or
+ * after every kv_len).  Its layout is the library's own: kie_kv4_read gives the
+ * values. */
+typedef struct {
+    void* data;
+    int32_t batch;
+    int32_t n_kv_heads;
+    int32_t max_ctx;      /* positions per request, at most 2^30 */
+    int32_t head_dim;     /* 64 or 128                           */
+    int32_t group;        /* 32, 64 or 128, at most head_dim     */
+    int32_t device;       /* CUDA device ordinal                 */
+} kie_kv4_cache;
+
+/* Bytes of c->data (0 for an invalid shape; data and device are not looked at). */
+size_t kie_kv4_bytes(const kie_kv4_cache* c);
+
+/* Store the K and V of new tokens: token t < n_tok[b] of request b goes to
+ * position start[b] + t; tokens whose position is outside [0, max_ctx) are
+ * dropped.  k, v: device [batch][n_tokens][n_kv_heads][head_dim] of `dtype`,
+ * the channels contiguous; k_strides, v_strides: NULL (contiguous) or host
+ * arrays of the three strides, in elements, between requests, tokens and heads
+ * (slices of a fused projection, broadcasts).  start: device int32 [batch];
+ * n_tok: NULL (n_tokens for every request) or device int32 [batch]. */
+kie_status kie_kv4_append(const kie_kv4_cache* c, const void* k, const void* v, int32_t dtype,
+                          const int64_t* k_strides, const int64_t* v_strides, int32_t n_tokens, const int32_t* start,
+                          const int32_t* n_tok, void* stream);
+
+/* The values stored at positions start[b] .. start[b] + n_tok[b] - 1, code * s +
+ * z in fp32 rounded to `dtype` (fp16 saturating), into k and v as kie_kv4_append
+ * lays them out.  Rows of tokens that it would not store are left as they are. */
+kie_status kie_kv4_read(const kie_kv4_cache* c, void* k, void* v, int32_t dtype, const int64_t* k_strides,
+                        const int64_t* v_strides, int32_t n_tokens, const int32_t* start, const int32_t* n_tok,
+                        void* stream);
+
+/* Attention of new tokens over the cache.  q and out: device
+ * [batch][n_tokens][n_heads][head_dim] of `dtype`, strides as for
+ * kie_kv4_append; query head h reads K/V head h / (n_heads / n_kv_heads).
+ * kv_len: device int32 [batch], the positions stored (clamped to [0, max_ctx]);
+ * n_tok: NULL (n_tokens) or device int32 [batch] (clamped to [0, n_tokens]):
+ * request b's queries are rows t < n_tok[b], the others of out are left as they
+ * are.  causal: query t sees the keys 0 .. kv_len[b] - n_tok[b] + t, and with
+ * window > 0 only the last `window` of them; not causal: all kv_len[b] (window
+ * must be 0).  A query that sees no key gives zeros.  out = softmax(scale q k^T)
+ * v over the values that the cache stands for; scores, softmax and sums in
+ * fp32.  scale must be finite. */
+typedef struct {
+    const void* q;
+    void* out;
+    const int64_t* q_strides;
+    const int64_t* out_strides;
+    const int32_t* kv_len;
+    const int32_t* n_tok;
+    int32_t dtype;
+    int32_t n_tokens;
+    int32_t n_heads;      /* a multiple of the cache's n_kv_heads */
+    int32_t causal;
+    int32_t window;
+    float scale;
+} kie_kv4_query;
+
+/* Device bytes that kie_kv4_attention needs for a query of this shape (dtype,
+ * n_tokens and n_heads are looked at); 0 for an invalid one. */
+size_t kie_kv4_attention_workspace(const kie_kv4_cache* c, const kie_kv4_query* q);
+
+/* workspace: device memory of at least kie_kv4_attention_workspace() bytes,
+ * 16-byte aligned, for this call alone until its work on `stream` is done. */
+kie_status kie_kv4_attention(const kie_kv4_cache* c, const kie_kv4_query* q, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* A token per row of logits from given random numbers.  logits: device
+ * [rows][vocab] of `dtype`, rows row_stride elements apart; temperature, top_k,
+ * top_p, min_p: NULL or device [rows]; u: device fp32 [rows] in [0, 1); tokens:
+ * device int32 [rows]; probs: NULL or device fp32 [rows].  Of each row, with m
+ * its largest logit and w_i = exp((l_i - m) / temperature):
+ *   temperature (NULL: 1): not above 0 means greedy, the lowest id of the
+ *     largest logit, with probability 1;
+ *   top_k (NULL, <= 0 or >= vocab: off): the first k in the order (logit
+ *     descending, id ascending);
+ *   top_p (NULL or >= 1: off): of those the shortest prefix with at least top_p
+ *     of their mass, and at least one token;
+ *   min_p (NULL or <= 0: off): of those the ones with w_i >= min(min_p, 1);
+ *   the token is the first, by id, at which the running mass of the kept ones
+ *     exceeds u times their total (u is taken as 0 below 0, and as the largest
+ *     number below 1 from 1 on); its probability is w / that total.
+ * (a difference m - l_i beyond fp32's range counts as infinite).  Masses are exact sums of weights in units of 2^-44, so results do not depend
+ * on how the work is split.  A logit of -infinity or NaN is never chosen;
+ * logits of +infinity share the mass; a row that leaves nothing gives token -1
+ * and probability 0.  vocab is at most 2^18. */
+typedef struct {
+    const void* logits;
+    int32_t dtype;
+    int32_t rows;
+    int32_t vocab;
+    int64_t row_stride;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* u;
+    int32_t* tokens;
+    float* probs;
+    int32_t device;
+} kie_sample_args;
+kie_status kie_sample(const kie_sample_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
