@@ -12,15 +12,18 @@
 // mantissa bits of an fp16 is the subnormal code * 2^-24 (2^-20 where it sits 4
 // bits higher), an exact operand that costs one AND for two codes.  The powers
 // of two move into q for K and to the end for V.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "kie_device.cuh"
 #include "kie_kv4.h"
 
 using namespace kie;
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -93,6 +96,16 @@ __device__ __forceinline__ bool place(const Kv4& c, int64_t r, int n, const int3
     return pos >= 0 && pos < c.max_ctx;
 }
 
+// Where the scale and the zero of a row's group lie, in fp16 elements of the params
+// (rows of a head start at multiples of 64, so a row's place in its block is row % 8).
+struct ParAt { size_t s, z; };
+__device__ __forceinline__ ParAt par_at(size_t row, int gi, int ng, bool isv) {
+    const size_t blk = (row >> 3) * (16 * ng);
+    const int r = int(row & 7), e = r >> 2, t = e ? 7 - r : r;
+    if (isv) return ParAt{blk + (t * 2 * ng + gi) * 2 + e, blk + (t * 2 * ng + ng + gi) * 2 + e};
+    return ParAt{row * (2 * ng) + gi, row * (2 * ng) + ng + gi};
+}
+
 // ---- store -------------------------------------------------------------------------------------
 // A row (one position of one head, K or V) is D/8 lanes with 8 channels each.
 template <int T, int D>
@@ -155,9 +168,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4 c, const void* k, c
     }
     const int ng = D / c.group, lpg = c.group / 8;
     if (ok && l % lpg == 0) {
-        uint16_t* pp = (isv ? c.vp : c.kp) + row * (2 * ng) + l / lpg;
-        pp[0] = __half_as_ushort(sh);
-        pp[ng] = __half_as_ushort(__float2half_rn(lo));
+        const ParAt at = par_at(row, l / lpg, ng, isv);
+        uint16_t* pp = isv ? c.vp : c.kp;
+        pp[at.s] = __half_as_ushort(sh);
+        pp[at.z] = __half_as_ushort(__float2half_rn(lo));
     }
 }
 
@@ -183,8 +197,9 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4 c, void* k, void* v, 
         w = uint32_t(u[0]) | uint32_t(u[BLK]) << 16;
     }
     const int ng = D / c.group, gi = l * 8 / c.group;
-    const uint16_t* pp = (isv ? c.vp : c.kp) + row * (2 * ng);
-    const float s = __half2float(__ushort_as_half(pp[gi])), z = __half2float(__ushort_as_half(pp[ng + gi]));
+    const ParAt at = par_at(row, gi, ng, isv);
+    const uint16_t* pp = isv ? c.vp : c.kp;
+    const float s = __half2float(__ushort_as_half(pp[at.s])), z = __half2float(__ushort_as_half(pp[at.z]));
     float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -197,18 +212,30 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4 c, void* k, void* v, 
 }
 
 // ---- attention ---------------------------------------------------------------------------------
-// Work is a list of tiles of TP positions: for every pair (request, tile of RT
-// query rows) and K/V head, the tiles that some row of it sees.  The list is cut
-// into equal ranges, one per CTA, whatever the requests' lengths; a CTA's range
-// meets one or more (pair, head) items and leaves a partial (m, l, o) of each
-// that it does not hold whole.  A second kernel joins the partials.
+// An item is a pair (request, tile of RT query rows) and a K/V head; its work is
+// the tiles of TP positions that some row of it sees.  Two forms:
+//   cluster  an item belongs to a cluster of CTAs that split its tiles and join
+//            their (m, l, o) through distributed shared memory: one launch;
+//   stream   the tiles of all items form one list that is cut into equal ranges,
+//            one per CTA, whatever the requests' lengths; a CTA leaves a partial
+//            (m, l, o) of each item that it does not hold whole, and a second
+//            kernel joins the partials.
 constexpr int TP = 32;        // positions per tile = one warp's step
-constexpr int NW = 8;         // warps per CTA, each with its own tiles and copies in flight
-constexpr int STG = 3;        // tiles in flight per warp
+#ifndef KV4_NW
+#define KV4_NW 8
+#define KV4_STG 2
+#endif
+constexpr int NW = KV4_NW;    // warps per CTA, each with its own tiles and copies in flight
+constexpr int STG = KV4_STG;  // tiles in flight per warp
+constexpr int CPS = 2;        // CTAs per SM
+constexpr int MAXS = 8;       // CTAs per cluster
 
-// HL8: 8 query rows, the operands q and p as fp16 hi + lo in rows r and r + 8
-// (22 bits and more: fp32 and fp16 tensors).  S8, S16: 8 or 16 rows, one fp16
-// each (bf16 tensors: 11 bits are 8 times finer than their rounding).
+// Both products run transposed, the cache as the 16-row operand and the query
+// rows as the 8 columns: S^T = K q^T, o^T = V^T p^T.  A warp's accumulators then
+// hold 8 rows and nothing else, and each unpacked code is used once.
+// HL8: 8 query rows, the operands q and p as fp16 hi + lo (22 bits and more: fp32
+// and fp16 tensors).  S8, S16: 8 or 16 rows, one fp16 each (bf16 tensors: 11 bits
+// are 8 times finer than their rounding).
 enum Mode { HL8 = 0, S8 = 1, S16 = 2 };
 __host__ __device__ constexpr int rows_of(int mode) { return mode == S16 ? 16 : 8; }
 
@@ -216,7 +243,7 @@ struct AttnArgs {
     Kv4Attn a;
     int32_t per;             // query heads per K/V head
     int32_t nrt;             // row tiles per request
-    int32_t nctas;           // CTAs of the main kernel
+    int32_t nctas;           // stream: CTAs of the main kernel; cluster: CTAs per item
 };
 
 // The keys that the rows [r0, r0 + rt) of request b see, as positions [lo, hi).
@@ -234,30 +261,32 @@ __device__ __forceinline__ void pair_keys(const AttnArgs& A, int b, int r0, int 
         if (lo >= hi) lo = hi = 0;
     }
 }
+__device__ __forceinline__ int key_tiles(int lo, int hi) { return hi > lo ? (hi + TP - 1) / TP - lo / TP : 0; }
 __device__ __forceinline__ int pair_tiles(const AttnArgs& A, int p, int rt) {
     int lo, hi, len, n;
     pair_keys(A, p / A.nrt, (p % A.nrt) * rt, rt, lo, hi, len, n);
-    return hi > lo ? (hi + TP - 1) / TP - lo / TP : 0;
+    return key_tiles(lo, hi);
 }
 
-// First tile of each CTA's range, of T tiles over n CTAs.
-__device__ __forceinline__ int64_t range_begin(int64_t T, int i, int n) { return T * i / n; }
+// First tile of CTA i's range, of T tiles over n CTAs (fewer than n where T is: no range is empty).
+__device__ __forceinline__ int list_ctas(int64_t T, int n) { return int(min(T, int64_t(n))); }
+__device__ __forceinline__ int64_t range_begin(int64_t T, int i, int n) { return i >= n ? T : T * i / n; }
 
-// One warp: total tiles, and the pair that holds tile `at` (with its first tile).
-__device__ __forceinline__ int64_t scan_pairs(const AttnArgs& A, int rt, int64_t at_num, int at_den, int& pair,
-                                              int64_t& first, int64_t& at) {
+// One warp: total tiles, and the pair that holds the first tile `at` of CTA i (with the pair's first tile).
+__device__ __forceinline__ int64_t scan_pairs(const AttnArgs& A, int rt, int i, int& pair, int64_t& first, int64_t& at) {
     const int lane = threadIdx.x & 31, np = A.a.c.batch * A.nrt;
-    int64_t T = 0;
-    for (int p0 = 0; p0 < np; p0 += 32) T += p0 + lane < np ? pair_tiles(A, p0 + lane, rt) : 0;
+    const int own0 = lane < np ? pair_tiles(A, lane, rt) : 0;     // the first 32 pairs, kept
+    int64_t T = own0;
+    for (int p0 = 32; p0 < np; p0 += 32) T += p0 + lane < np ? pair_tiles(A, p0 + lane, rt) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
     T *= A.a.c.heads;
-    at = T * at_num / at_den;
+    at = range_begin(T, i, list_ctas(T, A.nctas));
     pair = np;
     first = T;
     int64_t run = 0;
     for (int p0 = 0; p0 < np; p0 += 32) {
-        const int64_t own = p0 + lane < np ? int64_t(pair_tiles(A, p0 + lane, rt)) * A.a.c.heads : 0;
+        const int64_t own = int64_t(p0 == 0 ? own0 : p0 + lane < np ? pair_tiles(A, p0 + lane, rt) : 0) * A.a.c.heads;
         int64_t inc = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -276,11 +305,18 @@ __device__ __forceinline__ int64_t scan_pairs(const AttnArgs& A, int rt, int64_t
     return T;
 }
 
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// The same onto a zero accumulator.
+__device__ __forceinline__ void mma16816_0(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -298,8 +334,10 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ float h_lo(uint32_t w) { return __half2float(__ushort_as_half(uint16_t(w))); }
+__device__ __forceinline__ float h_hi(uint32_t w) { return __half2float(__ushort_as_half(uint16_t(w >> 16))); }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
-// Four codes pairs of a word whose halves hold two elements' nibbles: element
+// Four code pairs of a word whose halves hold two elements' nibbles: element
 // values code * 2^-24 * {1, 16, 1, 16}.
 __device__ __forceinline__ void unpack4(uint32_t w, uint32_t* r) {
     r[0] = w & 0x000F000Fu;
@@ -307,9 +345,24 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t* r) {
     r[2] = (w >> 8) & 0x000F000Fu;
     r[3] = (w >> 8) & 0x00F000F0u;
 }
-// 16-byte copy global -> shared of the first n (0..16) bytes, zeros after them.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// Transpose of the warp's 8 x 8 fp16 matrix (lane 4r + c holds row r, columns 2c and 2c + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int D, int NG>
@@ -317,87 +370,118 @@ struct Tile {
     static constexpr int CODES = TP * D / 2, PAR = TP * 4 * NG, BYTES = 2 * (CODES + PAR);
 };
 
-// The NG scales (or zeros) of a position, as floats.
+// NG consecutive words (one load).
+template <int NG> struct Words { uint32_t w[NG]; };
 template <int NG>
-__device__ __forceinline__ void scales(const uint8_t* par, int pos, float* s) {
-    if (NG == 4) {
-        const uint2 w = *reinterpret_cast<const uint2*>(par + pos * 16);
-        const float2 a = h2_to_f2(w.x), b = h2_to_f2(w.y);
-        s[0] = a.x; s[1] = a.y; s[2 % NG] = b.x; s[3 % NG] = b.y;
-    } else if (NG == 2) {
-        const float2 a = h2_to_f2(*reinterpret_cast<const uint32_t*>(par + pos * 8));
-        s[0] = a.x; s[1 % NG] = a.y;
+__device__ __forceinline__ Words<NG> load_words(const uint8_t* p) {
+    Words<NG> r;
+    if constexpr (NG == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if constexpr (NG == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = v.x; r.w[1] = v.y;
     } else {
-        s[0] = h2_to_f2(*reinterpret_cast<const uint32_t*>(par + pos * 4)).x;
+        r.w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
+    return r;
 }
 
-template <int D, int NG, int MODE, int T>
-__global__ void __launch_bounds__(NW * 32, 1) kv4_attention_kernel(const AttnArgs A) {
+// What the warps of a CTA share, after their rings.
+template <int D, int NG, int MODE>
+struct AttnShared {
+    static constexpr int RT = rows_of(MODE), BLK = D / 32;
+    uint4 q[BLK][MODE == S8 ? 1 : 2][32];   // operands of q: [block][rows + 8 (S16) or rest (HL8)][lane], two mmas each
+    float qmax[BLK][16];          // row maxima of |q| per block
+    float qsum[BLK][16];          // row sums of q per block
+    float part[RT * (D + 2)];     // cluster: this CTA's o [RT][D], then (m, l) [RT]
+    int64_t plan[4];
+};
+
+template <int D, int NG, int MODE, int T, bool CLUSTER>
+__global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnArgs A) {
     using E = typename Elem<T>::type;
     using TL = Tile<D, NG>;
     constexpr int RT = rows_of(MODE), BLK = D / 32, BPG = BLK / NG;   // 32-channel blocks, per group
-    constexpr int RPL = MODE == S16 ? 2 : 1;                          // query rows per lane
+    constexpr int NT = RT / 8;                                        // tiles of 8 query rows
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_plan[4];
+    AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
+    uint8_t* const pool = smem + (sizeof(S) + 127) / 128 * 128;       // rings, then merge buffer
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint8_t* ring = smem + warp * (STG * TL::BYTES);
+    uint8_t* ring = pool + warp * (STG * TL::BYTES);
     const uint32_t ring_u = smem_u32(ring);
     const Kv4& c = A.a.c;
 
-    if (warp == 0) {
-        int pair;
-        int64_t first, at;
-        const int64_t total = scan_pairs(A, RT, blockIdx.x, A.nctas, pair, first, at);
-        const int64_t end = range_begin(total, blockIdx.x + 1, A.nctas);
-        if (lane == 0) { s_plan[0] = at; s_plan[1] = end; s_plan[2] = pair; s_plan[3] = first; }
+    int pair = 0, head = 0;
+    const int rank = CLUSTER ? int(blockIdx.x) % A.nctas : 0;
+    if (CLUSTER) {
+        const int item = int(blockIdx.x) / A.nctas;
+        pair = item / c.heads;
+        head = item % c.heads;
+    } else {
+        if (warp == 0) {
+            int64_t f, x;
+            int p;
+            const int64_t total = scan_pairs(A, RT, blockIdx.x, p, f, x);
+            if (lane == 0) {
+                S.plan[0] = x;
+                S.plan[1] = range_begin(total, blockIdx.x + 1, list_ctas(total, A.nctas));
+                S.plan[2] = p;
+                S.plan[3] = f;
+            }
+        }
+        __syncthreads();
+        // let the joining kernel's blocks come up: they wait for this grid's end
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-    __syncthreads();
-    // let the joining kernel's blocks come up: they wait for this grid's end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int64_t at = s_plan[0];
-    const int64_t end = s_plan[1];
-    int pair = int(s_plan[2]);
-    int64_t first = s_plan[3];       // first tile of the pair
-    while (at < end) {
-        const int nt = pair_tiles(A, pair, RT);
-        if (at >= first + int64_t(nt) * c.heads) { first += int64_t(nt) * c.heads; ++pair; continue; }
-        const int head = int((at - first) / nt);
-        const int tile0 = int((at - first) % nt);
-        const int ntile = int(min(int64_t(nt - tile0), end - at));
-        at += ntile;
+    // stream: the list's state (next tile, end, pair, the pair's first tile) stays in S.plan
+    while (true) {
+        if (!CLUSTER) {
+            if (S.plan[0] >= S.plan[1]) break;
+            pair = int(S.plan[2]);
+        }
         const int b = pair / A.nrt, r0 = (pair % A.nrt) * RT;
         int lo, hi, len, n_new;
         pair_keys(A, b, r0, RT, lo, hi, len, n_new);
+        const int nt = key_tiles(lo, hi);
+        int tile0, ntile;
+        if (CLUSTER) {
+            if (r0 >= n_new * A.per) return;          // no such rows: the whole cluster leaves
+            tile0 = int(int64_t(nt) * rank / A.nctas);
+            ntile = int(int64_t(nt) * (rank + 1) / A.nctas) - tile0;
+        } else {
+            const int64_t at = S.plan[0], first = S.plan[3], pt = int64_t(nt) * c.heads;
+            if (at >= first + pt) {
+                __syncthreads();
+                if (threadIdx.x == 0) { S.plan[2] = pair + 1; S.plan[3] = first + pt; }
+                __syncthreads();
+                continue;
+            }
+            head = int((at - first) / nt);
+            tile0 = int((at - first) - int64_t(head) * nt);
+            ntile = int(min(int64_t(nt - tile0), S.plan[1] - at));
+        }
         const int base = lo / TP * TP + tile0 * TP;           // first position of this segment
         const size_t row0 = (size_t(b) * c.heads + head) * c.ctx_pad;
-        const uint8_t* src[4] = {c.kc + row0 * (D / 2), c.vc + row0 * (D / 2),
-                                 reinterpret_cast<const uint8_t*>(c.kp) + row0 * (4 * NG),
-                                 reinterpret_cast<const uint8_t*>(c.vp) + row0 * (4 * NG)};
-        // copies of tile i of the segment into ring stage st; positions from len on become zeros
-        auto copy_tile = [&](int i, int st) {
-            const int p0 = base + i * TP, nv = min(TP, len - p0);   // valid positions (> 0)
-            const uint32_t dst = ring_u + st * TL::BYTES;
+        // this lane's 16-byte pieces of the tiles; V's land with halves of rows 2, 3, 6 and 7
+        // of each block swapped (D = 128), which spreads their reads over the banks
+        const uint8_t* const kcs = c.kc + (row0 + base) * (D / 2) + lane * 16;
+        const uint8_t* const vcs = c.vc + (row0 + base) * (D / 2) + lane * 16;
+        const uint8_t* const kps = reinterpret_cast<const uint8_t*>(c.kp) + (row0 + base) * (4 * NG) + lane * 16;
+        const uint8_t* const vps = reinterpret_cast<const uint8_t*>(c.vp) + (row0 + base) * (4 * NG) + lane * 16;
+        const uint32_t kdst = ring_u + lane * 16;
+        const uint32_t vdst = ring_u + TL::CODES + (D == 128 ? (lane * 16) ^ ((lane & 8) << 2) : lane * 16);
+        auto copy_tile = [&](int i, int st) {      // tile i of the segment into ring stage st
+            const size_t off = size_t(i) * TL::CODES;
+            const uint32_t d = st * TL::BYTES;
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const uint8_t* gsrc = src[a] + size_t(p0) * (D / 2);
-                const int nb = nv * (D / 2);
-#pragma unroll
-                for (int j = 0; j < TL::CODES / 512; ++j) {
-                    const int o = (j * 32 + lane) * 16;
-                    copy16(dst + a * TL::CODES + o, gsrc + o, o < nb ? 16 : 0);
-                }
+            for (int j = 0; j < TL::CODES / 512; ++j) {
+                copy16(kdst + d + j * 512, kcs + off + j * 512);
+                copy16(vdst + d + j * 512, vcs + off + j * 512);
             }
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const uint8_t* gsrc = src[2 + a] + size_t(p0) * (4 * NG);
-                const int nb = nv * (4 * NG);
-#pragma unroll
-                for (int j = 0; j < (TL::PAR + 511) / 512; ++j) {
-                    const int o = (j * 32 + lane) * 16;
-                    if (o < TL::PAR)
-                        copy16(dst + 2 * TL::CODES + a * TL::PAR + o, gsrc + o, min(16, max(0, nb - o)));
-                }
+            if (lane < TL::PAR / 16) {
+                copy16(kdst + d + 2 * TL::CODES, kps + size_t(i) * TL::PAR);
+                copy16(kdst + d + 2 * TL::CODES + TL::PAR, vps + size_t(i) * TL::PAR);
             }
         };
 #pragma unroll
@@ -406,99 +490,114 @@ __global__ void __launch_bounds__(NW * 32, 1) kv4_attention_kernel(const AttnArg
             cp_async_commit();
         }
 
-        // ---- this lane's query rows as operands
-        uint32_t qa[BLK][2][4];        // [block][mma][a0..a3]
-        uint32_t qz[2];                // sums of q over the groups: a0, a1 of the zeros' mma
-        float cq[RPL];                 // from the mma's units to log2 units of the softmax
-        int last[RPL], firstk[RPL];    // keys the row sees: firstk .. last
+        // ---- the query rows as operands: warp i prepares block i, lane (g, t) of it
+        // channels 8t .. 8t + 7 of rows g (and g + 8)
+        float qx[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r0 + g + nt * 8;
+            if (warp < BLK) {
+                const bool have = r < n_new * A.per;
+                const int tok = have ? r / A.per : 0, hq = head * A.per + (have ? r - tok * A.per : 0);
+                const E* p = static_cast<const E*>(A.a.q) + b * A.a.qs.b + tok * A.a.qs.t + hq * A.a.qs.h + warp * 32 + t * 8;
+                if (have) load8<T>(p, aligned16(p), qx[nt]);
+                float mx = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (!have) qx[nt][j] = 0.f;
+                    mx = fmaxf(mx, fabsf(qx[nt][j]));
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                if (t == 0) S.qmax[warp][g + nt * 8] = mx;
+            }
+        }
+        __syncthreads();
+        auto row_exp = [&](int row) {      // exponent of the row's largest element
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < BLK; ++i) mx = fmaxf(mx, S.qmax[i][row]);
+            return min(max(((__float_as_int(mx) >> 23) & 255) - 127, -100), 114);
+        };
+        if (warp < BLK) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // exact power of two that brings the row's largest element to [2^11, 2^12)
+                const float up = copysignf(pow2i(11 - row_exp(g + nt * 8)), A.a.scale);
+                float sum = 0.f;
+                uint32_t hi2[4], lo2[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // operand slot j pairs channels j and j + 4; the odd slots' codes are 16 times as large
+                    const float y0 = qx[nt][j] * up, y1 = qx[nt][j + 4] * up;
+                    const float f = (j & 1) ? 1.f / 16.f : 1.f;
+                    sum += y0 + y1;
+                    const float h0 = __half2float(__float2half_rn(y0)), h1 = __half2float(__float2half_rn(y1));
+                    hi2[j] = pack_h2(h0 * f, h1 * f);
+                    lo2[j] = pack_h2((y0 - h0) * f, (y1 - h1) * f);
+                }
+                S.q[warp][nt][lane] = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
+                if (MODE == HL8) S.q[warp][MODE == HL8 ? 1 : 0][lane] = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (t == 0) S.qsum[warp][g + nt * 8] = sum * (1.f / 256.f);
+            }
+        }
+        __syncthreads();
+        // the zeros' operand of row g: k = 2t, 2t+1 are a pair of groups (NG == 1: scale and
+        // zero), the sums' fp16 for t < 2, their rest after
+        uint32_t qz[NT];
+        float2 cq[NT];                 // rows 2t, 2t+1: from the mma's units to log2 units of the softmax
+        int last[NT][2], firstk[NT][2];     // keys they see: firstk .. last
         int all_lo = 0, all_hi = 1 << 30;   // positions that every row of the tile sees
 #pragma unroll
-        for (int rr = 0; rr < RPL; ++rr) {
-            const int r = r0 + g + rr * 8;
-            const bool have = r < n_new * A.per;
-            const int tok = have ? r / A.per : 0, hq = head * A.per + (have ? r % A.per : 0);
-            last[rr] = !have ? -1 : A.a.causal ? len - n_new + tok : len - 1;
-            firstk[rr] = A.a.window > 0 && A.a.causal ? last[rr] - A.a.window + 1 : 0;
-            if (have) { all_lo = max(all_lo, firstk[rr]); all_hi = min(all_hi, last[rr]); }
-            const E* qp = static_cast<const E*>(A.a.q) + b * A.a.qs.b + tok * A.a.qs.t + hq * A.a.qs.h;
-            float x[BLK][8], mx = 0.f, sum[NG];
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) sum[gi] = 0.f;
-#pragma unroll
-            for (int i = 0; i < BLK; ++i) {
-                const E* p = qp + i * 32 + t * 8;
-                if (have) load8<T>(p, aligned16(p), x[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (!have) x[i][j] = 0.f;
-                    mx = fmaxf(mx, fabsf(x[i][j]));
-                }
-            }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // exact power of two that brings the row's largest element to [2^11, 2^12)
-            int e = ((__float_as_int(mx) >> 23) & 255) - 127;
-            e = min(max(e, -100), 114);
-            const float up = pow2i(11 - e);
-            cq[rr] = A.a.scale * 1.4426950408889634f * pow2i(e - 11 + 24);
-#pragma unroll
-            for (int i = 0; i < BLK; ++i) {
-                float hi_[8], lo_[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float y = x[i][j] * up;
-                    sum[i / BPG] += y;
-                    hi_[j] = __half2float(__float2half_rn(y));
-                    lo_[j] = y - hi_[j];
-                    const float f = (j & 1) ? 1.f / 16.f : 1.f;
-                    hi_[j] *= f;
-                    lo_[j] *= f;
-                }
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int j = 2 * m + s;
-                        const uint32_t h2 = pack_h2(hi_[j], hi_[j + 4]);
-                        if (MODE == S16) qa[i][m][2 * s + rr] = h2;
-                        else {
-                            qa[i][m][2 * s] = h2;
-                            qa[i][m][2 * s + 1] = MODE == HL8 ? pack_h2(lo_[j], lo_[j + 4]) : 0u;
-                        }
-                    }
-            }
-            // zeros' operand: k = 2t', 2t'+1 are a pair of groups, hi for t' < 2, lo after
+        for (int nt = 0; nt < NT; ++nt) {
+            float sum[NG];
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-                sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 1);
-                sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 2);
-                sum[gi] *= 1.f / 256.f;
+                sum[gi] = 0.f;
+#pragma unroll
+                for (int j = 0; j < BPG; ++j) sum[gi] += S.qsum[gi * BPG + j][g + nt * 8];
             }
             float s0 = 0.f, s1 = 0.f;
             if (NG == 4) { s0 = (t & 1) ? sum[2 % NG] : sum[0]; s1 = (t & 1) ? sum[3 % NG] : sum[1 % NG]; }
             if (NG == 2 && (t & 1) == 0) { s0 = sum[0]; s1 = sum[1 % NG]; }
-            if (NG == 1 && (t & 1) == 0) s1 = sum[0];     // the pair is (scale, zero)
+            if (NG == 1 && (t & 1) == 0) s1 = sum[0];
             const float h0 = __half2float(__float2half_rn(s0)), h1 = __half2float(__float2half_rn(s1));
-            const uint32_t zz = t < 2 ? pack_h2(h0, h1) : pack_h2(s0 - h0, s1 - h1);
-            qz[rr] = zz;
-            if (RPL == 1) qz[1] = 0u;
+            qz[nt] = t < 2 ? pack_h2(h0, h1) : pack_h2(s0 - h0, s1 - h1);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 2 * t + e + nt * 8, r = r0 + row;
+                const bool have = r < n_new * A.per;
+                last[nt][e] = !have ? -1 : A.a.causal ? len - n_new + r / A.per : len - 1;
+                firstk[nt][e] = A.a.window > 0 && A.a.causal ? last[nt][e] - A.a.window + 1 : 0;
+                if (have) { all_lo = max(all_lo, firstk[nt][e]); all_hi = min(all_hi, last[nt][e]); }
+                // above 0: it keeps -inf
+                (e ? cq[nt].y : cq[nt].x) = fmaxf(fabsf(A.a.scale) * 1.4426950408889634f * pow2i(row_exp(row) - 11 + 24), 1.2e-38f);
+            }
         }
-        const int zoff = NG == 4 ? 8 + (t & 1) * 4 : NG == 2 ? 4 : 0;
-
-        float o[BLK][4][4];            // [block][nibble][c0..c3]
-        float zl[4] = {0.f, 0.f, 0.f, 0.f};
-        float m[RPL];
-        int ev = 1;                    // biased fp16 exponent of the largest V scale so far
-#pragma unroll
-        for (int i = 0; i < BLK; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[i][j][k] = 0.f;
-#pragma unroll
-        for (int rr = 0; rr < RPL; ++rr) m[rr] = -INFINITY;
         all_lo = __reduce_max_sync(0xffffffffu, all_lo);
         all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+        // this lane's places in a block of 8 positions: K row of operand row g, V rows t and 7 - t
+        const int krow = g & 1 ? 7 - (g >> 1) : g >> 1;
+        const int koff = krow * (D / 2) + t * (D / 8);
+        const int v0off = t * (D / 2) + (D == 128 ? (g * 8) ^ ((t & 2) << 4) : g * 4);
+        const int v1off = (7 - t) * (D / 2) + (D == 128 ? (g * 8) ^ (((7 - t) & 2) << 4) : g * 4);
+
+        float o[NT][BLK][2][4];        // o^T: [block][nibbles 2jj (c0, c1) and 2jj + 1 (c2, c3)], columns 2t, 2t + 1
+        float zl[NT][4];               // row g < NG: sum of p z of group g, row NG: sum of p
+        float2 m[NT];
+        int ev = 1;                    // biased fp16 exponent of the largest V scale so far
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                zl[nt][k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < BLK; ++i) o[nt][i][0][k] = o[nt][i][1][k] = 0.f;
+            }
+        }
 
         int st = 0;
         for (int i = warp; i < ntile; i += NW) {
@@ -518,191 +617,201 @@ __global__ void __launch_bounds__(NW * 32, 1) kv4_attention_kernel(const AttnArg
             const uint8_t* vp = kp + TL::PAR;
             if (++st == STG) st = 0;
             const int p0 = base + i * TP;
-
-            // ---- scores of 32 positions: x[tile][row][2]
-            float x[4][RPL][2];
+            if (p0 + TP > len) {       // parameters that nothing was stored to: zeros for V (K's scores are masked)
+                if (p0 + lane >= len) {
+                    uint16_t* v = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(vp));
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) {
+                        const ParAt at = par_at(lane, gi, NG, true);
+                        v[at.s] = 0;
+                        v[at.z] = 0;
+                    }
+                }
+                __syncwarp();
+            }
+            // ---- scores of 2 x 16 positions, in units of cq: x[half][block][tile] = rows (2t, 2t+1) of position krow
+            float2 x[2][2][NT];
+            Words<BLK> w[4];
+            Words<NG> par[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const int pos = n * 8 + g;
-                uint32_t w[BLK];
-                if (D == 128) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(kc + pos * 64 + t * 16);
-                    w[0] = v.x; w[1] = v.y; w[2 % BLK] = v.z; w[3 % BLK] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(kc + pos * 32 + t * 8);
-                    w[0] = v.x; w[1] = v.y;
+                w[n] = load_words<BLK>(kc + n * 4 * D + koff);
+                par[n] = load_words<NG>(kp + (n * 8 + krow) * 4 * NG);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                auto zero = [&](const Words<NG>& q) { return NG == 4 ? ((t & 1) ? q.w[3 % NG] : q.w[2 % NG]) : q.w[NG - 1]; };
+                const uint4 az = make_uint4(zero(par[2 * hh]), zero(par[2 * hh + 1]), 0u, 0u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float z[4];
+                    mma16816_0(z, az, qz[nt], 0u);
+                    x[hh][0][nt] = make_float2(z[0] * (1.f / 65536.f), z[1] * (1.f / 65536.f));
+                    x[hh][1][nt] = make_float2(z[2] * (1.f / 65536.f), z[3] * (1.f / 65536.f));
                 }
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint32_t az[4] = {qz[0], qz[1], 0u, 0u};
-                mma16816(z, az, *reinterpret_cast<const uint32_t*>(kp + pos * 4 * NG + zoff), 0u);
-                float s0[NG], s1[NG];
-                scales<NG>(kp, n * 8 + 2 * t, s0);
-                scales<NG>(kp, n * 8 + 2 * t + 1, s1);
-                float y[RPL][2];
+            }
 #pragma unroll
-                for (int rr = 0; rr < RPL; ++rr) {
-                    y[rr][0] = z[2 * rr] * (1.f / 65536.f);
-                    y[rr][1] = z[2 * rr + 1] * (1.f / 65536.f);
-                }
+            for (int gi = 0; gi < NG; ++gi) {
+                float acc[2][NT][4];
 #pragma unroll
-                for (int gi = 0; gi < NG; ++gi) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < BPG; ++j) {
+                    const int i2 = gi * BPG + j;
+                    uint4 qf[NT], ql;
 #pragma unroll
-                    for (int j = 0; j < BPG; ++j) {
-                        uint32_t r[4];
-                        unpack4(w[gi * BPG + j], r);
-                        mma16816(acc, qa[gi * BPG + j][0], r[0], r[1]);
-                        mma16816(acc, qa[gi * BPG + j][1], r[2], r[3]);
+                    for (int nt = 0; nt < NT; ++nt) qf[nt] = S.q[i2][nt][lane];
+                    if (MODE == HL8) ql = S.q[i2][MODE == HL8 ? 1 : 0][lane];
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t ra[4], rb[4];
+                        unpack4(w[2 * hh].w[i2], ra);
+                        unpack4(w[2 * hh + 1].w[i2], rb);
+                        const uint4 a0 = make_uint4(ra[0], rb[0], ra[1], rb[1]), a1 = make_uint4(ra[2], rb[2], ra[3], rb[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (j == 0) mma16816_0(acc[hh][nt], a0, qf[nt].x, qf[nt].y);
+                            else mma16816(acc[hh][nt], a0, qf[nt].x, qf[nt].y);
+                            mma16816(acc[hh][nt], a1, qf[nt].z, qf[nt].w);
+                        }
+                        if (MODE == HL8) {
+                            mma16816(acc[hh][0], a0, ql.x, ql.y);
+                            mma16816(acc[hh][0], a1, ql.z, ql.w);
+                        }
                     }
-                    if (MODE == HL8) { acc[0] += acc[2]; acc[1] += acc[3]; }
+                }
 #pragma unroll
-                    for (int rr = 0; rr < RPL; ++rr) {
-                        y[rr][0] = fmaf(acc[2 * rr], s0[gi], y[rr][0]);
-                        y[rr][1] = fmaf(acc[2 * rr + 1], s1[gi], y[rr][1]);
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t sw = par[2 * hh + k].w[gi >> 1];
+                        const float s = gi & 1 ? h_hi(sw) : h_lo(sw);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            x[hh][k][nt] = __ffma2_rn(make_float2(acc[hh][nt][2 * k], acc[hh][nt][2 * k + 1]), make_float2(s, s), x[hh][k][nt]);
                     }
-                }
-#pragma unroll
-                for (int rr = 0; rr < RPL; ++rr) {
-                    x[n][rr][0] = y[rr][0] * cq[rr];
-                    x[n][rr][1] = y[rr][1] * cq[rr];
-                }
             }
             if (p0 < all_lo || p0 + TP - 1 > all_hi) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-                    for (int rr = 0; rr < RPL; ++rr)
+                    for (int k = 0; k < 2; ++k) {
+                        const int p = p0 + hh * 16 + k * 8 + krow;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int p = p0 + n * 8 + 2 * t + k;
-                            if (p < firstk[rr] || p > last[rr]) x[n][rr][k] = -INFINITY;
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (p < firstk[nt][0] || p > last[nt][0]) x[hh][k][nt].x = -INFINITY;
+                            if (p < firstk[nt][1] || p > last[nt][1]) x[hh][k][nt].y = -INFINITY;
                         }
+                    }
             }
             // ---- running maximum, and the largest V scale of the tile
-            float corr[RPL], mref[RPL];
+            float2 corr[NT], mref[NT];
             bool grew = false;
 #pragma unroll
-            for (int rr = 0; rr < RPL; ++rr) {
-                float mx = x[0][rr][0];
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 mx = x[0][0][nt];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) mx = max_nan(mx, max_nan(x[n][rr][0], x[n][rr][1]));
-                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = max_nan(m[rr], mx);
-                grew |= mn > m[rr];
-                mref[rr] = (mn == -INFINITY ? 0.f : mn) - 15.f;      // p <= 2^15: fp16's range, used whole
-                corr[rr] = ex2(m[rr] - 15.f - mref[rr]);
-                m[rr] = mn;
+                for (int k = 1; k < 4; ++k) {
+                    mx.x = max_nan(mx.x, x[k >> 1][k & 1][nt].x);
+                    mx.y = max_nan(mx.y, x[k >> 1][k & 1][nt].y);
+                }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    mx.x = max_nan(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, d));
+                    mx.y = max_nan(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, d));
+                }
+                const float2 mn = make_float2(max_nan(m[nt].x, mx.x * cq[nt].x), max_nan(m[nt].y, mx.y * cq[nt].y));
+                grew |= mn.x > m[nt].x || mn.y > m[nt].y;
+                // p <= 2^15: fp16's range, used whole
+                mref[nt] = make_float2((mn.x == -INFINITY ? 0.f : mn.x) - 15.f, (mn.y == -INFINITY ? 0.f : mn.y) - 15.f);
+                corr[nt] = make_float2(ex2(m[nt].x - 15.f - mref[nt].x), ex2(m[nt].y - 15.f - mref[nt].y));
+                m[nt] = mn;
             }
             uint32_t sb;
-            if (NG == 4) {
-                const uint2 w = *reinterpret_cast<const uint2*>(vp + lane * 16);
-                const uint32_t a = __vmaxu2(w.x, w.y);
+            {
+                const Words<NG> v = load_words<NG>(vp + (lane & 15) * 8 * NG);   // pair lane % 16 of the tile
+                uint32_t a = v.w[0];
+#pragma unroll
+                for (int gi = 1; gi < NG; ++gi) a = __vmaxu2(a, v.w[gi]);
                 sb = max(a & 0xFFFFu, a >> 16);
-            } else if (NG == 2) {
-                const uint32_t a = *reinterpret_cast<const uint32_t*>(vp + lane * 8);
-                sb = max(a & 0xFFFFu, a >> 16);
-            } else {
-                sb = *reinterpret_cast<const uint32_t*>(vp + lane * 4) & 0xFFFFu;
             }
             const int en = max(ev, int(__reduce_max_sync(0xffffffffu, sb) >> 10));
             if (__any_sync(0xffffffffu, grew) || en > ev) {
                 const float fe = pow2i(ev - en);
                 ev = en;
 #pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    const float cz = corr[RPL == 2 ? rr : 0], co = cz * fe;
-                    zl[2 * rr] *= cz;
-                    zl[2 * rr + 1] *= cz;
+                for (int nt = 0; nt < NT; ++nt) {
+                    zl[nt][0] *= corr[nt].x;
+                    zl[nt][1] *= corr[nt].y;
+                    const float cx = corr[nt].x * fe, cy = corr[nt].y * fe;
 #pragma unroll
                     for (int i2 = 0; i2 < BLK; ++i2)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) { o[i2][j][2 * rr] *= co; o[i2][j][2 * rr + 1] *= co; }
+                        for (int j = 0; j < 2; ++j) {
+                            o[nt][i2][j][0] *= cx; o[nt][i2][j][1] *= cy;
+                            o[nt][i2][j][2] *= cx; o[nt][i2][j][3] *= cy;
+                        }
                 }
             }
             const float fv = pow2i(14 - ev);    // 2^-(E+1), E = ev - 15: p * s * fv < 2^15
-            // ---- o += p v, 16 positions at a time
+            const uint32_t fv2 = pack_h2(fv, fv);
+            // ---- o^T += v^T p^T, 16 positions at a time
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                const int pp[4] = {hh * 16 + 2 * t, hh * 16 + 2 * t + 1, hh * 16 + 8 + 2 * t, hh * 16 + 9 + 2 * t};
-                float p[RPL][4];
+                const uint8_t* va = vc + hh * 8 * D, *vb = va + 4 * D;          // codes and params of the two blocks
+                const uint8_t* pa = vp + hh * 64 * NG + t * 8 * NG, *pb = pa + 32 * NG;
+                // p as the operand: row g, positions (t, 7 - t) of the two blocks
+                uint32_t ph[NT][2], pl[2];
 #pragma unroll
-                for (int rr = 0; rr < RPL; ++rr)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) p[rr][k] = ex2(x[2 * hh + (k >> 1)][rr][k & 1] - mref[rr]);
-                // zeros and the row sum: columns 0..NG-1 are the groups' zeros, column NG is 1
-                {
-                    uint32_t a[4];
-                    if (MODE == S16) {
-#pragma unroll
-                        for (int rr = 0; rr < RPL; ++rr) { a[rr] = pack_h2(p[rr][0], p[rr][1]); a[2 + rr] = pack_h2(p[rr][2], p[rr][3]); }
-                    } else {
-                        a[0] = pack_h2(p[0][0], p[0][1]);
-                        a[2] = pack_h2(p[0][2], p[0][3]);
-                        a[1] = a[3] = 0u;
-                        if (MODE == HL8) {
-                            const float2 h0 = h2_to_f2(a[0]), h1 = h2_to_f2(a[2]);
-                            a[1] = pack_h2(p[0][0] - h0.x, p[0][1] - h0.y);
-                            a[3] = pack_h2(p[0][2] - h1.x, p[0][3] - h1.y);
-                        }
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 y = x[hh][k][nt];
+                        const float px = ex2(fmaf(y.x, cq[nt].x, -mref[nt].x)), py = ex2(fmaf(y.y, cq[nt].y, -mref[nt].y));
+                        const uint32_t h = pack_h2(px, py);
+                        ph[nt][k] = transpose8(h);
+                        if (MODE == HL8) pl[k] = transpose8(pack_h2(px - h_lo(h), py - h_hi(h)));
                     }
-                    uint32_t b0 = g == NG ? 0x3C003C00u : 0u, b1 = b0;
+                {   // zeros and the row sum: rows 0..NG-1 are the groups' zeros, row NG is 1
+                    uint32_t z0 = g == NG ? 0x3C003C00u : 0u, z1 = z0;
                     if (g < NG) {
-                        const uint8_t* zp = vp + 2 * NG + 2 * g;
-                        auto zh = [&](int q) { return uint32_t(*reinterpret_cast<const uint16_t*>(zp + pp[q] * 4 * NG)); };
-                        b0 = zh(0) | zh(1) << 16;
-                        b1 = zh(2) | zh(3) << 16;
+                        z0 = *reinterpret_cast<const uint32_t*>(pa + 4 * NG + 4 * g);
+                        z1 = *reinterpret_cast<const uint32_t*>(pb + 4 * NG + 4 * g);
                     }
-                    mma16816(zl, a, b0, b1);
+                    const uint4 az = make_uint4(z0, 0u, z1, 0u);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(zl[nt], az, ph[nt][0], ph[nt][1]);
+                    if (MODE == HL8) mma16816(zl[0], az, pl[0], pl[1]);
                 }
-                float sv[4][NG];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) scales<NG>(vp, pp[k], sv[k]);
-#pragma unroll
-                for (int rr = 0; rr < RPL; ++rr)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) p[rr][k] *= fv;
-                uint32_t vw[4][D / 64];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (D == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(vc + pp[k] * 64 + g * 8);
-                        vw[k][0] = v.x; vw[k][1 % (D / 64)] = v.y;
-                    } else {
-                        vw[k][0] = *reinterpret_cast<const uint32_t*>(vc + pp[k] * 32 + g * 4);
-                    }
-                }
-                uint32_t a[4];
+                const Words<NG> sa = load_words<NG>(pa), sb2 = load_words<NG>(pb);
+                Words<D / 64> vw[4];
+                vw[0] = load_words<D / 64>(va + v0off);
+                vw[1] = load_words<D / 64>(va + v1off);
+                vw[2] = load_words<D / 64>(vb + v0off);
+                vw[3] = load_words<D / 64>(vb + v1off);
+                uint32_t b[NT][2], bl[2];
 #pragma unroll
                 for (int i2 = 0; i2 < BLK; ++i2) {
-                    if (i2 % BPG == 0) {     // p * s of the group
-                        const int gi = i2 / BPG;
+                    if (i2 % BPG == 0) {     // p * s of the group, below 2^15
+                        const uint32_t s[2] = {hmul2(sa.w[i2 / BPG], fv2), hmul2(sb2.w[i2 / BPG], fv2)};   // exact, below 1
 #pragma unroll
-                        for (int rr = 0; rr < RPL; ++rr) {
-                            const float y0 = p[rr][0] * sv[0][gi], y1 = p[rr][1] * sv[1][gi];
-                            const float y2 = p[rr][2] * sv[2][gi], y3 = p[rr][3] * sv[3][gi];
-                            if (MODE == S16) {
-                                a[rr] = pack_h2(y0, y1);
-                                a[2 + rr] = pack_h2(y2, y3);
-                            } else {
-                                a[0] = pack_h2(y0, y1);
-                                a[2] = pack_h2(y2, y3);
-                                a[1] = a[3] = 0u;
-                                if (MODE == HL8) {
-                                    const float2 h0 = h2_to_f2(a[0]), h1 = h2_to_f2(a[2]);
-                                    a[1] = pack_h2(y0 - h0.x, y1 - h0.y);
-                                    a[3] = pack_h2(y2 - h1.x, y3 - h1.y);
-                                }
-                            }
+                        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) b[nt][k] = hmul2(ph[nt][k], s[k]);
+                            // the product's rest is exact in fp16; the low part's product joins it
+                            if (MODE == HL8) bl[k] = hfma2(pl[k], s[k], hfma2(ph[0][k], s[k], b[0][k] ^ 0x80008000u));
                         }
                     }
                     const int wi = i2 >> 1;
                     const uint32_t sel = (i2 & 1) ? 0x7632u : 0x5410u;
-                    uint32_t r0_[4], r1_[4];
-                    unpack4(__byte_perm(vw[0][wi], vw[1][wi], sel), r0_);
-                    unpack4(__byte_perm(vw[2][wi], vw[3][wi], sel), r1_);
+                    uint32_t u0[4], u1[4];
+                    unpack4(__byte_perm(vw[0].w[wi], vw[1].w[wi], sel), u0);
+                    unpack4(__byte_perm(vw[2].w[wi], vw[3].w[wi], sel), u1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mma16816(o[i2][j], a, r0_[j], r1_[j]);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 a = make_uint4(u0[2 * j], u0[2 * j + 1], u1[2 * j], u1[2 * j + 1]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i2][j], a, b[nt][0], b[nt][1]);
+                        if (MODE == HL8) mma16816(o[0][i2][j], a, bl[0], bl[1]);
+                    }
                 }
             }
         }
@@ -710,69 +819,98 @@ __global__ void __launch_bounds__(NW * 32, 1) kv4_attention_kernel(const AttnArg
         __syncthreads();               // every warp is done with its ring: it becomes the merge buffer
 
         // ---- merge the warps: [warp][RT][D] sums, [warp][RT][8] zeros and row sums, [warp][RT] maxima
-        float* mo = reinterpret_cast<float*>(smem);
+        float* mo = reinterpret_cast<float*>(pool);
         float* mz = mo + NW * RT * D;
         float* mm = mz + NW * RT * 8;
-        const float back = pow2i(ev - 14) * 16777216.f;   // undo fv and the codes' 2^-24
+        const int nw = min(NW, ntile);                    // warps that had a tile
+        if (warp < nw) {
+            const float back = pow2i(ev - 14) * 16777216.f;   // undo fv and the codes' 2^-24
 #pragma unroll
-        for (int rr = 0; rr < RPL; ++rr) {
-            const int row = warp * RT + g + rr * 8;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < BLK; ++i)
+                for (int e = 0; e < 2; ++e) {
+                    const int row = warp * RT + nt * 8 + 2 * t + e;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float4 v;
-                    float* e = &v.x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float y = MODE == HL8 ? o[i][j][k] + o[i][j][2 + k] : o[i][j][2 * rr + k];
-                        e[j] = y * (back * ((j & 1) ? 1.f / 16.f : 1.f));
-                    }
-                    *reinterpret_cast<float4*>(mo + size_t(row) * D + i * 32 + t * 8 + k * 4) = v;
+                    for (int i = 0; i < BLK; ++i)
+                        *reinterpret_cast<float4*>(mo + size_t(row) * D + i * 32 + g * 4) =
+                            make_float4(o[nt][i][0][e] * back, o[nt][i][0][2 + e] * (back * 0.0625f),
+                                        o[nt][i][1][e] * back, o[nt][i][1][2 + e] * (back * 0.0625f));
+                    mz[row * 8 + g] = zl[nt][e];
+                    if (g == 0) mm[row] = e ? m[nt].y : m[nt].x;
                 }
-            mz[row * 8 + 2 * t] = MODE == HL8 ? zl[0] + zl[2] : zl[2 * rr];
-            mz[row * 8 + 2 * t + 1] = MODE == HL8 ? zl[1] + zl[3] : zl[2 * rr + 1];
-            if (t == 0) mm[row] = m[rr];
         }
         __syncthreads();
-        const bool whole = ntile == nt;
-        float* part = A.a.ws + (size_t(pair) * c.heads + head + blockIdx.x) * (RT * (D + 2));
+        const bool whole = CLUSTER ? A.nctas == 1 : ntile == nt;
+        float* part = CLUSTER ? S.part : A.a.ws + (size_t(pair) * c.heads + head + blockIdx.x) * (RT * (D + 2));
+        auto store = [&](int i, float os, float ls) {
+            const int row = r0 + i / D;
+            if (row < n_new * A.per) {
+                const int tok = row / A.per;
+                E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + tok * A.a.os.t + (head * A.per + row - tok * A.per) * A.a.os.h;
+                op[i % D] = Elem<T>::from(ls == 0.f ? 0.f : os / ls);
+            }
+        };
         for (int i = threadIdx.x; i < RT * D; i += NW * 32) {
             const int r = i / D, d = i % D;
             float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) M = max_nan(M, mm[w * RT + r]);
+            for (int w = 0; w < nw; ++w) M = max_nan(M, mm[w * RT + r]);
             float os = 0.f, ls = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
+            for (int w = 0; w < nw; ++w) {
                 const float mw = mm[w * RT + r];
                 const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
                 os = fmaf(f, mo[(w * RT + r) * D + d] + mz[(w * RT + r) * 8 + d / (D / NG)], os);
                 ls = fmaf(f, mz[(w * RT + r) * 8 + NG], ls);
             }
             if (whole) {
-                const int row = r0 + r;
-                if (row < n_new * A.per) {
-                    E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + (row / A.per) * A.a.os.t +
-                            (head * A.per + row % A.per) * A.a.os.h;
-                    op[d] = Elem<T>::from(ls == 0.f ? 0.f : os / ls);
-                }
+                store(i, os, ls);
             } else {
                 part[i] = os;
                 if (d == 0) { part[RT * D + 2 * r] = M; part[RT * D + 2 * r + 1] = ls; }
             }
         }
+        if (CLUSTER && A.nctas > 1) {
+            // join the CTAs' parts: CTA `rank` does every nctas-th stretch of the elements
+            cg::cluster_group cl = cg::this_cluster();
+            cl.sync();
+            const float* parts[MAXS];
+#pragma unroll
+            for (int k = 0; k < MAXS; ++k) parts[k] = cl.map_shared_rank(S.part, k < A.nctas ? k : 0);
+            const int per = RT * D / A.nctas;
+            for (int j = threadIdx.x; j < per; j += NW * 32) {
+                const int i = rank * per + j, r = i / D;
+                float M = -INFINITY, mk[MAXS], lk[MAXS], ok[MAXS];
+#pragma unroll
+                for (int k = 0; k < MAXS; ++k) {
+                    mk[k] = k < A.nctas ? parts[k][RT * D + 2 * r] : -INFINITY;
+                    lk[k] = k < A.nctas ? parts[k][RT * D + 2 * r + 1] : 0.f;
+                    ok[k] = k < A.nctas ? parts[k][i] : 0.f;
+                    M = max_nan(M, mk[k]);
+                }
+                float os = 0.f, ls = 0.f;
+#pragma unroll
+                for (int k = 0; k < MAXS; ++k) {
+                    const float f = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - M);
+                    os = fmaf(f, ok[k], os);
+                    ls = fmaf(f, lk[k], ls);
+                }
+                store(i, os, ls);
+            }
+            cl.sync();                 // no CTA leaves while another may read its part
+        }
+        if (CLUSTER) break;
+        if (threadIdx.x == 0) S.plan[0] += ntile;
         __syncthreads();               // the merge buffer becomes the ring again
     }
 }
 
 // Join the partials of every item that more than one CTA worked on; items
-// without a key get zeros.  One block per (pair, K/V head).
+// without a key get zeros.  One block per (pair, K/V head) and 256 elements.
 template <int D, int RT, int T>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs A) {
     using E = typename Elem<T>::type;
-    __shared__ int64_t s_at[3];
-    const int pair = blockIdx.x / A.a.c.heads, head = blockIdx.x % A.a.c.heads;
+    __shared__ int64_t s_at[2];
+    constexpr int PER = RT * D / 256;
+    const int item = blockIdx.x / PER, pair = item / A.a.c.heads, head = item % A.a.c.heads;
     if (threadIdx.x < 32) {
         // tiles of the pairs before this one, and of all
         const int np = A.a.c.batch * A.nrt;
@@ -790,49 +928,61 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs A) {
         if (threadIdx.x == 0) { s_at[0] = before * A.a.c.heads; s_at[1] = T_ * A.a.c.heads; }
     }
     __syncthreads();
-    // every block waits for the main kernel, also one with nothing to join: what
-    // follows in the stream waits for this kernel alone
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t total = s_at[1];
     int lo, hi, len, n_new;
     const int b = pair / A.nrt, r0 = (pair % A.nrt) * RT;
     pair_keys(A, b, r0, RT, lo, hi, len, n_new);
-    const int rows = min(RT, n_new * A.per - r0);
-    if (rows <= 0) return;
-    const int nt = pair_tiles(A, pair, RT);
-    const int64_t t0 = s_at[0] + int64_t(head) * nt, t1 = t0 + nt;
+    const int i = int(blockIdx.x % PER) * 256 + threadIdx.x, r = i / D, d = i % D, row = r0 + r;
+    const int nt = key_tiles(lo, hi);
     int c0 = 0, c1 = 0;                 // CTAs c0 .. c1 hold tiles of this item
     if (nt > 0) {
+        const int64_t t0 = s_at[0] + int64_t(head) * nt, t1 = t0 + nt;
+        const int n = list_ctas(total, A.nctas);
         // CTA of tile x: the largest i with total * i / n <= x
         auto owner = [&](int64_t x) {
-            int64_t i = (x * A.nctas) / total;
-            while (i + 1 < A.nctas && range_begin(total, int(i + 1), A.nctas) <= x) ++i;
-            while (i > 0 && range_begin(total, int(i), A.nctas) > x) --i;
-            return int(i);
+            int k = int((x * n) / total);
+            while (k + 1 < n && range_begin(total, k + 1, n) <= x) ++k;
+            while (k > 0 && range_begin(total, k, n) > x) --k;
+            return k;
         };
         c0 = owner(t0);
         c1 = owner(t1 - 1);
-        if (c0 == c1) return;           // one CTA held it whole and wrote the result
     }
+    // every block waits for the main kernel, also one with nothing to join: what
+    // follows in the stream waits for this kernel alone
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= n_new * A.per || (nt > 0 && c0 == c1)) return;   // one CTA held it whole and wrote the result
     const float* part = A.a.ws + (size_t(pair) * A.a.c.heads + head) * (RT * (D + 2));
-    for (int i = threadIdx.x; i < rows * D; i += 256) {
-        const int r = i / D, d = i % D;
-        float M = -INFINITY, ls = 0.f, os = 0.f;
-        if (nt > 0)
-            for (int k = c0; k <= c1; ++k) {
-                if (range_begin(total, k, A.nctas) == range_begin(total, k + 1, A.nctas)) continue;   // an empty range
-                const float* pk = part + size_t(k) * (RT * (D + 2));
-                const float mk = __ldcg(pk + RT * D + 2 * r);
-                if (mk == -INFINITY) continue;
-                const float mn = max_nan(M, mk), f0 = ex2(M - mn), f1 = ex2(mk - mn);
-                ls = ls * f0 + __ldcg(pk + RT * D + 2 * r + 1) * f1;
-                os = os * f0 + __ldcg(pk + i) * f1;
-                M = mn;
-            }
-        const int row = r0 + r;
-        E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + (row / A.per) * A.a.os.t + (head * A.per + row % A.per) * A.a.os.h;
-        op[d] = Elem<T>::from(ls == 0.f ? 0.f : os / ls);
+    float M = -INFINITY, ls = 0.f, os = 0.f;
+    constexpr int U = 8;                // partials in flight
+    for (int k0 = c0; nt > 0 && k0 <= c1; k0 += U) {
+        float mk[U], lk[U], ok[U], mn = M;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float* pk = part + size_t(min(k0 + k, c1)) * (RT * (D + 2));
+            mk[k] = __ldcg(pk + RT * D + 2 * r);
+            lk[k] = __ldcg(pk + RT * D + 2 * r + 1);
+            ok[k] = __ldcg(pk + i);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (k0 + k > c1) mk[k] = -INFINITY;
+            mn = max_nan(mn, mk[k]);
+        }
+        const float f = M == -INFINITY ? 0.f : ex2(M - mn);
+        ls *= f;
+        os *= f;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float fk = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - mn);
+            ls = fmaf(lk[k], fk, ls);
+            os = fmaf(ok[k], fk, os);
+        }
+        M = mn;
     }
+    const int tok = row / A.per;
+    E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + tok * A.a.os.t + (head * A.per + row - tok * A.per) * A.a.os.h;
+    op[d] = Elem<T>::from(ls == 0.f ? 0.f : os / ls);
 }
 
 int mode_of(int type, int rows) { return type != KV4_BF16 ? HL8 : rows <= 8 ? S8 : S16; }
@@ -851,33 +1001,55 @@ cudaError_t opt_in(K* kernel, int bytes, std::atomic<uint64_t>& done) {
 }
 
 template <int D, int NG, int MODE, int T>
-cudaError_t launch_attention(const AttnArgs& A, cudaStream_t st) {
+cudaError_t launch_attention(AttnArgs A, int sms, cudaStream_t st) {
     constexpr int RT = rows_of(MODE);
     constexpr int ring = NW * STG * Tile<D, NG>::BYTES, merge = NW * RT * (D + 9) * 4;
-    constexpr int smem = ring > merge ? ring : merge;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t r = opt_in(kv4_attention_kernel<D, NG, MODE, T>, smem, done);
-    if (r != cudaSuccess) return r;
-    kv4_attention_kernel<D, NG, MODE, T><<<A.nctas, NW * 32, smem, st>>>(A);
-    r = cudaGetLastError();
-    if (r != cudaSuccess) return r;
+    constexpr int smem = (int(sizeof(AttnShared<D, NG, MODE>)) + 127) / 128 * 128 + (ring > merge ? ring : merge);
+    static std::atomic<uint64_t> done{0}, done_c{0};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(A.a.c.batch) * A.nrt * A.a.c.heads);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    // The most tiles an item can have, by what the host knows.
+    const int64_t items = int64_t(A.a.c.batch) * A.nrt * A.a.c.heads;
+    int64_t keys = A.a.c.max_ctx;
+    if (A.a.window > 0) keys = std::min<int64_t>(keys, int64_t(A.a.window) + (RT + A.per - 1) / A.per + TP);
+    const int64_t tiles = (keys + TP - 1) / TP;
+    // Cluster form: while a warp has few tiles, the second launch and the list's
+    // set-up cost more than an uneven split.
+    if (items * tiles <= int64_t(sms) * CPS * NW * 4) {
+        int S = 1;
+        while (S < MAXS && S * NW < tiles && items * S * 2 <= sms * CPS) S *= 2;
+        A.nctas = S;
+        cudaError_t r = opt_in(kv4_attention_kernel<D, NG, MODE, T, true>, smem, done_c);
+        if (r != cudaSuccess) return r;
+        cfg.gridDim = dim3(unsigned(items * S));
+        cfg.blockDim = dim3(NW * 32);
+        cfg.dynamicSmemBytes = smem;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = S;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        return cudaLaunchKernelEx(&cfg, kv4_attention_kernel<D, NG, MODE, T, true>, A);
+    }
+    cudaError_t r = opt_in(kv4_attention_kernel<D, NG, MODE, T, false>, smem, done);
+    if (r != cudaSuccess) return r;
+    kv4_attention_kernel<D, NG, MODE, T, false><<<A.nctas, NW * 32, smem, st>>>(A);
+    r = cudaGetLastError();
+    if (r != cudaSuccess) return r;
+    cfg.gridDim = dim3(unsigned(items * (RT * D / 256)));
+    cfg.blockDim = dim3(256);
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, RT, T>, A);
 }
 
 template <int D, int NG>
-cudaError_t launch_attention_t(const AttnArgs& A, int mode, cudaStream_t st) {
-    if (A.a.type == KV4_F16) return launch_attention<D, NG, HL8, KV4_F16>(A, st);
-    if (A.a.type == KV4_F32) return launch_attention<D, NG, HL8, KV4_F32>(A, st);
-    return mode == S8 ? launch_attention<D, NG, S8, KV4_BF16>(A, st) : launch_attention<D, NG, S16, KV4_BF16>(A, st);
+cudaError_t launch_attention_t(const AttnArgs& A, int mode, int sms, cudaStream_t st) {
+    if (A.a.type == KV4_F16) return launch_attention<D, NG, HL8, KV4_F16>(A, sms, st);
+    if (A.a.type == KV4_F32) return launch_attention<D, NG, HL8, KV4_F32>(A, sms, st);
+    return mode == S8 ? launch_attention<D, NG, S8, KV4_BF16>(A, sms, st) : launch_attention<D, NG, S16, KV4_BF16>(A, sms, st);
 }
 
 template <int T>
@@ -923,7 +1095,7 @@ extern "C" size_t kie_kv4_attention_ws_floats(const Kv4* c, int heads, int n_q, 
     const int64_t rows = int64_t(n_q) * (heads / c->heads);
     const int rt = rows_of(mode_of(type, rows > 8 ? 16 : 8));
     const size_t items = size_t(c->batch) * size_t((rows + rt - 1) / rt) * c->heads;
-    return (items + size_t(sms)) * rt * (c->dim + 2);
+    return (items + size_t(sms) * CPS) * rt * (c->dim + 2);
 }
 
 extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaStream_t st) {
@@ -933,13 +1105,13 @@ extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaS
     const int64_t rows = int64_t(a->n_q) * A.per;
     const int mode = mode_of(a->type, rows > 8 ? 16 : 8);
     A.nrt = int((rows + rows_of(mode) - 1) / rows_of(mode));
-    A.nctas = sms;
+    A.nctas = sms * CPS;
     const int ng = a->c.dim / a->c.group;
     if (a->c.dim == 128) {
-        if (ng == 4) return launch_attention_t<128, 4>(A, mode, st);
-        if (ng == 2) return launch_attention_t<128, 2>(A, mode, st);
-        return launch_attention_t<128, 1>(A, mode, st);
+        if (ng == 4) return launch_attention_t<128, 4>(A, mode, sms, st);
+        if (ng == 2) return launch_attention_t<128, 2>(A, mode, sms, st);
+        return launch_attention_t<128, 1>(A, mode, sms, st);
     }
-    if (ng == 2) return launch_attention_t<64, 2>(A, mode, st);
-    return launch_attention_t<64, 1>(A, mode, st);
+    if (ng == 2) return launch_attention_t<64, 2>(A, mode, sms, st);
+    return launch_attention_t<64, 1>(A, mode, sms, st);
 }

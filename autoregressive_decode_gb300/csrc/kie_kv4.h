@@ -8,18 +8,24 @@
 // pairs, K and V apart:
 //
 //   codes  [batch][head][ctx_pad][D/8] 32-bit words
-//   params [batch][head][ctx_pad][2][D/g] fp16: the scales, then the zeros
+//   params [batch][head][ctx_pad/8] blocks of 8 positions, 32 D/g bytes each
 //
 // ctx_pad is max_ctx rounded up to 64 positions, so that every head starts on a
-// 256-byte boundary and 16-byte copies never straddle two heads.
+// 256-byte boundary and whole tiles of positions lie inside the head's memory.
 //
-// Codes are stored in the order in which a warp's matrix fragments take them,
-// so that one vector load per lane feeds whole m16n8k16 operands:
+// Codes and params are stored in the order in which a warp's matrix fragments
+// take them, so that one vector load per lane feeds whole m16n8k16 operands:
 //   K word t*(D/32) + b holds channels 32b + 8t + n in nibble n (t = 0..3): lane
 //     t of a quad reads its D/32 words, one per 32-channel block, in one load;
 //   V 16-bit unit g*(D/32) + b holds channels 32b + 4g + n in nibble n (g = 0..7):
 //     lane group g reads its units of a position in one load, and two positions'
-//     units merge into the (position, position + 1) pairs of an operand.
+//     units merge into the pairs of an operand;
+//   row 2t + e of an operand's 8 positions is position t of the block (e = 0) or
+//     7 - t (e = 1): the pairs (0,7) (1,6) (2,5) (3,4) read the codes without bank
+//     conflicts;
+//   K block: per position its fp16 scales, then its zeros;
+//   V block: per pair t words [group] of the scales, then of the zeros (positions
+//     run along the operand there).
 struct Kv4 {
     uint8_t *kc, *vc;        // codes
     uint16_t *kp, *vp;       // params, fp16 bits
