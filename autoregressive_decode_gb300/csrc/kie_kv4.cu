@@ -63,6 +63,20 @@ __device__ __forceinline__ void load8(const typename Elem<T>::type* p, bool vec,
         for (int j = 0; j < 8; ++j) f[j] = Elem<T>::to(p[j]);
     }
 }
+// N (2 or 4) consecutive channels, vectorised where the address allows.
+template <int T, int N>
+__device__ __forceinline__ void load_few(const typename Elem<T>::type* p, float* f) {
+    using E = typename Elem<T>::type;
+    struct alignas(N * sizeof(E)) V { E e[N]; };
+    V v;
+    if ((reinterpret_cast<uintptr_t>(p) & (sizeof(V) - 1)) == 0) v = *reinterpret_cast<const V*>(p);
+    else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v.e[j] = p[j];
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = Elem<T>::to(v.e[j]);
+}
 template <int T>
 __device__ __forceinline__ void store8(typename Elem<T>::type* p, bool vec, const float* f) {
     using E = typename Elem<T>::type;
@@ -227,7 +241,6 @@ constexpr int TP = 32;        // positions per tile = one warp's step
 #endif
 constexpr int NW = KV4_NW;    // warps per CTA, each with its own tiles and copies in flight
 constexpr int STG = KV4_STG;  // tiles in flight per warp
-constexpr int CPS = 2;        // CTAs per SM
 constexpr int MAXS = 8;       // CTAs per cluster
 
 // Both products run transposed, the cache as the 16-row operand and the query
@@ -238,6 +251,8 @@ constexpr int MAXS = 8;       // CTAs per cluster
 // are 8 times finer than their rounding).
 enum Mode { HL8 = 0, S8 = 1, S16 = 2 };
 __host__ __device__ constexpr int rows_of(int mode) { return mode == S16 ? 16 : 8; }
+// CTAs per SM: 128 registers a thread do for all but 16 rows of 128 channels.
+__host__ __device__ constexpr int ctas_per_sm(int mode, int dim) { return mode == S16 && dim == 128 ? 1 : 2; }
 
 struct AttnArgs {
     Kv4Attn a;
@@ -392,14 +407,15 @@ template <int D, int NG, int MODE>
 struct AttnShared {
     static constexpr int RT = rows_of(MODE), BLK = D / 32;
     uint4 q[BLK][MODE == S8 ? 1 : 2][32];   // operands of q: [block][rows + 8 (S16) or rest (HL8)][lane], two mmas each
-    float qmax[BLK][16];          // row maxima of |q| per block
-    float qsum[BLK][16];          // row sums of q per block
-    float part[RT * (D + 2)];     // cluster: this CTA's o [RT][D], then (m, l) [RT]
+    float qsum[BLK][RT];          // row sums of q per block
+    int32_t qexp[RT];             // exponents of the rows' largest elements
+    float recv[RT * D];           // cluster: [CTA][RT * D / CTAs] sums of this CTA's stretch of the elements
+    float2 recv_ml[MAXS][RT];     // and every CTA's (m, l) of the rows
     int64_t plan[4];
 };
 
 template <int D, int NG, int MODE, int T, bool CLUSTER>
-__global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnArgs A) {
+__global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_kernel(const AttnArgs A) {
     using E = typename Elem<T>::type;
     using TL = Tile<D, NG>;
     constexpr int RT = rows_of(MODE), BLK = D / 32, BPG = BLK / NG;   // 32-channel blocks, per group
@@ -415,6 +431,7 @@ __global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnA
     int pair = 0, head = 0;
     const int rank = CLUSTER ? int(blockIdx.x) % A.nctas : 0;
     if (CLUSTER) {
+        if (A.nctas > 1) cg::this_cluster().barrier_arrive();   // waited for before the first remote write
         const int item = int(blockIdx.x) / A.nctas;
         pair = item / c.heads;
         head = item % c.heads;
@@ -441,12 +458,32 @@ __global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnA
             pair = int(S.plan[2]);
         }
         const int b = pair / A.nrt, r0 = (pair % A.nrt) * RT;
+        // ---- the query rows: warp w holds row w (and w + NW), a lane EPL channels; loaded first,
+        // their latency passes with that of the lengths
+        constexpr int EPL = D / 32, RPW = (RT + NW - 1) / NW;
+        float qx[RPW][EPL];
+        auto load_q = [&]() {
+#pragma unroll
+            for (int k = 0; k < RPW; ++k) {
+                const int r = r0 + warp + k * NW;
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) qx[k][j] = 0.f;
+                if (warp + k * NW < RT && r < A.a.n_q * A.per) {
+                    const int tok = r / A.per, hq = head * A.per + r - tok * A.per;
+                    load_few<T, EPL>(static_cast<const E*>(A.a.q) + b * A.a.qs.b + tok * A.a.qs.t + hq * A.a.qs.h + lane * EPL, qx[k]);
+                }
+            }
+        };
+        if (CLUSTER) load_q();
         int lo, hi, len, n_new;
         pair_keys(A, b, r0, RT, lo, hi, len, n_new);
         const int nt = key_tiles(lo, hi);
         int tile0, ntile;
         if (CLUSTER) {
-            if (r0 >= n_new * A.per) return;          // no such rows: the whole cluster leaves
+            if (r0 >= n_new * A.per) {                // no such rows: the whole cluster leaves
+                if (A.nctas > 1) cg::this_cluster().barrier_wait();
+                return;
+            }
             tile0 = int(int64_t(nt) * rank / A.nctas);
             ntile = int(int64_t(nt) * (rank + 1) / A.nctas) - tile0;
         } else {
@@ -460,6 +497,7 @@ __global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnA
             head = int((at - first) / nt);
             tile0 = int((at - first) - int64_t(head) * nt);
             ntile = int(min(int64_t(nt - tile0), S.plan[1] - at));
+            load_q();
         }
         const int base = lo / TP * TP + tile0 * TP;           // first position of this segment
         const size_t row0 = (size_t(b) * c.heads + head) * c.ctx_pad;
@@ -490,57 +528,40 @@ __global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnA
             cp_async_commit();
         }
 
-        // ---- the query rows as operands: warp i prepares block i, lane (g, t) of it
-        // channels 8t .. 8t + 7 of rows g (and g + 8)
-        float qx[NT][8];
+        // ---- the query rows as operands
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = r0 + g + nt * 8;
-            if (warp < BLK) {
-                const bool have = r < n_new * A.per;
-                const int tok = have ? r / A.per : 0, hq = head * A.per + (have ? r - tok * A.per : 0);
-                const E* p = static_cast<const E*>(A.a.q) + b * A.a.qs.b + tok * A.a.qs.t + hq * A.a.qs.h + warp * 32 + t * 8;
-                if (have) load8<T>(p, aligned16(p), qx[nt]);
+        for (int k = 0; k < RPW; ++k) {
+            const int row = warp + k * NW;
+            if (row < RT) {                           // uniform over the warp
+                const bool have = r0 + row < n_new * A.per;
                 float mx = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (!have) qx[nt][j] = 0.f;
-                    mx = fmaxf(mx, fabsf(qx[nt][j]));
+                for (int j = 0; j < EPL; ++j) {
+                    if (!have) qx[k][j] = 0.f;
+                    mx = fmaxf(mx, fabsf(qx[k][j]));
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                if (t == 0) S.qmax[warp][g + nt * 8] = mx;
-            }
-        }
-        __syncthreads();
-        auto row_exp = [&](int row) {      // exponent of the row's largest element
-            float mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < BLK; ++i) mx = fmaxf(mx, S.qmax[i][row]);
-            return min(max(((__float_as_int(mx) >> 23) & 255) - 127, -100), 114);
-        };
-        if (warp < BLK) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
                 // exact power of two that brings the row's largest element to [2^11, 2^12)
-                const float up = copysignf(pow2i(11 - row_exp(g + nt * 8)), A.a.scale);
+                const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+                const int e = min(max(int(mb >> 23) - 127, -100), 114);
+                const float up = copysignf(pow2i(11 - e), A.a.scale);
+                // channel 32 i + 8 tt + j: half j >> 2 of slot j & 3 of block i, lane (row, tt); the odd
+                // slots' codes are 16 times as large
+                const int d0 = lane * EPL, i = d0 >> 5, tt = (d0 >> 3) & 3;
                 float sum = 0.f;
-                uint32_t hi2[4], lo2[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // operand slot j pairs channels j and j + 4; the odd slots' codes are 16 times as large
-                    const float y0 = qx[nt][j] * up, y1 = qx[nt][j + 4] * up;
-                    const float f = (j & 1) ? 1.f / 16.f : 1.f;
-                    sum += y0 + y1;
-                    const float h0 = __half2float(__float2half_rn(y0)), h1 = __half2float(__float2half_rn(y1));
-                    hi2[j] = pack_h2(h0 * f, h1 * f);
-                    lo2[j] = pack_h2((y0 - h0) * f, (y1 - h1) * f);
+                for (int j = 0; j < EPL; ++j) {
+                    const float y = qx[k][j] * up, h = __half2float(__float2half_rn(y));
+                    const int s8 = (d0 + j) & 7;
+                    const float f = (s8 & 1) ? 1.f / 16.f : 1.f;
+                    sum += y;
+                    reinterpret_cast<__half*>(&S.q[i][row >> 3][4 * (row & 7) + tt])[2 * (s8 & 3) + (s8 >> 2)] = __float2half_rn(h * f);
+                    if (MODE == HL8)
+                        reinterpret_cast<__half*>(&S.q[i][MODE == HL8 ? 1 : 0][4 * row + tt])[2 * (s8 & 3) + (s8 >> 2)] = __float2half_rn((y - h) * f);
                 }
-                S.q[warp][nt][lane] = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
-                if (MODE == HL8) S.q[warp][MODE == HL8 ? 1 : 0][lane] = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (t == 0) S.qsum[warp][g + nt * 8] = sum * (1.f / 256.f);
+#pragma unroll
+                for (int d = 1; d < 32 / EPL; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);   // over the block's lanes
+                if ((d0 & 31) == 0) S.qsum[i][row] = sum * (1.f / 256.f);
+                if (lane == 0) S.qexp[row] = e;
             }
         }
         __syncthreads();
@@ -573,7 +594,7 @@ __global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnA
                 firstk[nt][e] = A.a.window > 0 && A.a.causal ? last[nt][e] - A.a.window + 1 : 0;
                 if (have) { all_lo = max(all_lo, firstk[nt][e]); all_hi = min(all_hi, last[nt][e]); }
                 // above 0: it keeps -inf
-                (e ? cq[nt].y : cq[nt].x) = fmaxf(fabsf(A.a.scale) * 1.4426950408889634f * pow2i(row_exp(row) - 11 + 24), 1.2e-38f);
+                (e ? cq[nt].y : cq[nt].x) = fmaxf(fabsf(A.a.scale) * 1.4426950408889634f * pow2i(S.qexp[row] - 11 + 24), 1.2e-38f);
             }
         }
         all_lo = __reduce_max_sync(0xffffffffu, all_lo);
@@ -822,80 +843,102 @@ __global__ void __launch_bounds__(NW * 32, CPS) kv4_attention_kernel(const AttnA
         float* mo = reinterpret_cast<float*>(pool);
         float* mz = mo + NW * RT * D;
         float* mm = mz + NW * RT * 8;
-        const int nw = min(NW, ntile);                    // warps that had a tile
-        if (warp < nw) {
+        {
             const float back = pow2i(ev - 14) * 16777216.f;   // undo fv and the codes' 2^-24
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt8 = 0; nt8 < NT; ++nt8)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int row = warp * RT + nt * 8 + 2 * t + e;
+                    const int row = warp * RT + nt8 * 8 + 2 * t + e;
 #pragma unroll
                     for (int i = 0; i < BLK; ++i)
                         *reinterpret_cast<float4*>(mo + size_t(row) * D + i * 32 + g * 4) =
-                            make_float4(o[nt][i][0][e] * back, o[nt][i][0][2 + e] * (back * 0.0625f),
-                                        o[nt][i][1][e] * back, o[nt][i][1][2 + e] * (back * 0.0625f));
-                    mz[row * 8 + g] = zl[nt][e];
-                    if (g == 0) mm[row] = e ? m[nt].y : m[nt].x;
+                            make_float4(o[nt8][i][0][e] * back, o[nt8][i][0][2 + e] * (back * 0.0625f),
+                                        o[nt8][i][1][e] * back, o[nt8][i][1][2 + e] * (back * 0.0625f));
+                    mz[row * 8 + g] = zl[nt8][e];
+                    if (g == 0) mm[row] = e ? m[nt8].y : m[nt8].x;
                 }
         }
         __syncthreads();
         const bool whole = CLUSTER ? A.nctas == 1 : ntile == nt;
-        float* part = CLUSTER ? S.part : A.a.ws + (size_t(pair) * c.heads + head + blockIdx.x) * (RT * (D + 2));
-        auto store = [&](int i, float os, float ls) {
-            const int row = r0 + i / D;
+        float* part = A.a.ws + (size_t(pair) * c.heads + head + blockIdx.x) * (RT * (D + 2));
+        // four channels of a row, by 1 / ls
+        auto store = [&](int r, int d, float4 v, float ls) {
+            const int row = r0 + r;
             if (row < n_new * A.per) {
                 const int tok = row / A.per;
-                E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + tok * A.a.os.t + (head * A.per + row - tok * A.per) * A.a.os.h;
-                op[i % D] = Elem<T>::from(ls == 0.f ? 0.f : os / ls);
+                E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + tok * A.a.os.t + (head * A.per + row - tok * A.per) * A.a.os.h + d;
+                const float f[4] = {v.x, v.y, v.z, v.w};
+                struct alignas(4 * sizeof(E)) V { E e[4]; } w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w.e[j] = Elem<T>::from(ls == 0.f ? 0.f : f[j] / ls);
+                if ((reinterpret_cast<uintptr_t>(op) & (sizeof(V) - 1)) == 0) *reinterpret_cast<V*>(op) = w;
+                else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) op[j] = w.e[j];
+                }
             }
         };
-        for (int i = threadIdx.x; i < RT * D; i += NW * 32) {
+        cg::cluster_group cl = cg::this_cluster();
+        if (CLUSTER && A.nctas > 1) cl.barrier_wait();        // every CTA of the cluster runs
+        const int per = CLUSTER ? RT * D / A.nctas : 1;       // elements that a CTA of the cluster joins
+        for (int i = threadIdx.x * 4; i < RT * D; i += NW * 128) {
             const int r = i / D, d = i % D;
-            float M = -INFINITY;
-            for (int w = 0; w < nw; ++w) M = max_nan(M, mm[w * RT + r]);
-            float os = 0.f, ls = 0.f;
-            for (int w = 0; w < nw; ++w) {
-                const float mw = mm[w * RT + r];
-                const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-                os = fmaf(f, mo[(w * RT + r) * D + d] + mz[(w * RT + r) * 8 + d / (D / NG)], os);
+            float M = -INFINITY, mw[NW];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) { mw[w] = mm[w * RT + r]; M = max_nan(M, mw[w]); }
+            float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+            float ls = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - M);
+                const float4 v = *reinterpret_cast<const float4*>(mo + (w * RT + r) * D + d);
+                const float z = mz[(w * RT + r) * 8 + d / (D / NG)];
                 ls = fmaf(f, mz[(w * RT + r) * 8 + NG], ls);
+                os.x = fmaf(f, v.x + z, os.x);
+                os.y = fmaf(f, v.y + z, os.y);
+                os.z = fmaf(f, v.z + z, os.z);
+                os.w = fmaf(f, v.w + z, os.w);
             }
             if (whole) {
-                store(i, os, ls);
+                store(r, d, os, ls);
+            } else if (CLUSTER) {      // to the CTA that joins these elements
+                *reinterpret_cast<float4*>(cl.map_shared_rank(S.recv, i / per) + rank * per + i % per) = os;
+                if (d < 4 * A.nctas) cl.map_shared_rank(&S, d / 4)->recv_ml[rank][r] = make_float2(M, ls);
             } else {
-                part[i] = os;
-                if (d == 0) { part[RT * D + 2 * r] = M; part[RT * D + 2 * r + 1] = ls; }
+                *reinterpret_cast<float2*>(part + i) = make_float2(os.x, os.y);
+                *reinterpret_cast<float2*>(part + i + 2) = make_float2(os.z, os.w);
+                if (d == 0) *reinterpret_cast<float2*>(part + RT * D + 2 * r) = make_float2(M, ls);
             }
         }
         if (CLUSTER && A.nctas > 1) {
-            // join the CTAs' parts: CTA `rank` does every nctas-th stretch of the elements
-            cg::cluster_group cl = cg::this_cluster();
             cl.sync();
-            const float* parts[MAXS];
-#pragma unroll
-            for (int k = 0; k < MAXS; ++k) parts[k] = cl.map_shared_rank(S.part, k < A.nctas ? k : 0);
-            const int per = RT * D / A.nctas;
-            for (int j = threadIdx.x; j < per; j += NW * 32) {
+            for (int j = threadIdx.x * 4; j < per; j += NW * 128) {
                 const int i = rank * per + j, r = i / D;
-                float M = -INFINITY, mk[MAXS], lk[MAXS], ok[MAXS];
+                float M = -INFINITY, mk[MAXS], lk[MAXS];
 #pragma unroll
                 for (int k = 0; k < MAXS; ++k) {
-                    mk[k] = k < A.nctas ? parts[k][RT * D + 2 * r] : -INFINITY;
-                    lk[k] = k < A.nctas ? parts[k][RT * D + 2 * r + 1] : 0.f;
-                    ok[k] = k < A.nctas ? parts[k][i] : 0.f;
+                    const float2 ml = k < A.nctas ? S.recv_ml[k][r] : make_float2(-INFINITY, 0.f);
+                    mk[k] = ml.x;
+                    lk[k] = ml.y;
                     M = max_nan(M, mk[k]);
                 }
-                float os = 0.f, ls = 0.f;
+                float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+                float ls = 0.f;
 #pragma unroll
                 for (int k = 0; k < MAXS; ++k) {
-                    const float f = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - M);
-                    os = fmaf(f, ok[k], os);
-                    ls = fmaf(f, lk[k], ls);
+                    if (k < A.nctas) {
+                        const float f = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - M);
+                        const float4 v = *reinterpret_cast<const float4*>(S.recv + k * per + j);
+                        ls = fmaf(f, lk[k], ls);
+                        os.x = fmaf(f, v.x, os.x);
+                        os.y = fmaf(f, v.y, os.y);
+                        os.z = fmaf(f, v.z, os.z);
+                        os.w = fmaf(f, v.w, os.w);
+                    }
                 }
-                store(i, os, ls);
+                store(r, i % D, os, ls);
             }
-            cl.sync();                 // no CTA leaves while another may read its part
         }
         if (CLUSTER) break;
         if (threadIdx.x == 0) S.plan[0] += ntile;
@@ -1001,7 +1044,7 @@ cudaError_t opt_in(K* kernel, int bytes, std::atomic<uint64_t>& done) {
 }
 
 template <int D, int NG, int MODE, int T>
-cudaError_t launch_attention(AttnArgs A, int sms, cudaStream_t st) {
+cudaError_t launch_attention(AttnArgs A, cudaStream_t st) {
     constexpr int RT = rows_of(MODE);
     constexpr int ring = NW * STG * Tile<D, NG>::BYTES, merge = NW * RT * (D + 9) * 4;
     constexpr int smem = (int(sizeof(AttnShared<D, NG, MODE>)) + 127) / 128 * 128 + (ring > merge ? ring : merge);
@@ -1018,9 +1061,9 @@ cudaError_t launch_attention(AttnArgs A, int sms, cudaStream_t st) {
     const int64_t tiles = (keys + TP - 1) / TP;
     // Cluster form: while a warp has few tiles, the second launch and the list's
     // set-up cost more than an uneven split.
-    if (items * tiles <= int64_t(sms) * CPS * NW * 4) {
+    if (items * tiles <= int64_t(A.nctas) * NW * 4) {
         int S = 1;
-        while (S < MAXS && S * NW < tiles && items * S * 2 <= sms * CPS) S *= 2;
+        while (S < MAXS && S * NW < tiles && items * S * 2 <= A.nctas) S *= 2;
         A.nctas = S;
         cudaError_t r = opt_in(kv4_attention_kernel<D, NG, MODE, T, true>, smem, done_c);
         if (r != cudaSuccess) return r;
@@ -1046,10 +1089,10 @@ cudaError_t launch_attention(AttnArgs A, int sms, cudaStream_t st) {
 }
 
 template <int D, int NG>
-cudaError_t launch_attention_t(const AttnArgs& A, int mode, int sms, cudaStream_t st) {
-    if (A.a.type == KV4_F16) return launch_attention<D, NG, HL8, KV4_F16>(A, sms, st);
-    if (A.a.type == KV4_F32) return launch_attention<D, NG, HL8, KV4_F32>(A, sms, st);
-    return mode == S8 ? launch_attention<D, NG, S8, KV4_BF16>(A, sms, st) : launch_attention<D, NG, S16, KV4_BF16>(A, sms, st);
+cudaError_t launch_attention_t(const AttnArgs& A, int mode, cudaStream_t st) {
+    if (A.a.type == KV4_F16) return launch_attention<D, NG, HL8, KV4_F16>(A, st);
+    if (A.a.type == KV4_F32) return launch_attention<D, NG, HL8, KV4_F32>(A, st);
+    return mode == S8 ? launch_attention<D, NG, S8, KV4_BF16>(A, st) : launch_attention<D, NG, S16, KV4_BF16>(A, st);
 }
 
 template <int T>
@@ -1093,9 +1136,9 @@ extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const
 // CTAs are both consecutive, so no two (item, CTA) pairs that meet share a slot.
 extern "C" size_t kie_kv4_attention_ws_floats(const Kv4* c, int heads, int n_q, int type, int sms) {
     const int64_t rows = int64_t(n_q) * (heads / c->heads);
-    const int rt = rows_of(mode_of(type, rows > 8 ? 16 : 8));
+    const int mode = mode_of(type, rows > 8 ? 16 : 8), rt = rows_of(mode);
     const size_t items = size_t(c->batch) * size_t((rows + rt - 1) / rt) * c->heads;
-    return (items + size_t(sms) * CPS) * rt * (c->dim + 2);
+    return (items + size_t(sms) * ctas_per_sm(mode, c->dim)) * rt * (c->dim + 2);
 }
 
 extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaStream_t st) {
@@ -1105,13 +1148,13 @@ extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaS
     const int64_t rows = int64_t(a->n_q) * A.per;
     const int mode = mode_of(a->type, rows > 8 ? 16 : 8);
     A.nrt = int((rows + rows_of(mode) - 1) / rows_of(mode));
-    A.nctas = sms * CPS;
+    A.nctas = sms * ctas_per_sm(mode, a->c.dim);
     const int ng = a->c.dim / a->c.group;
     if (a->c.dim == 128) {
-        if (ng == 4) return launch_attention_t<128, 4>(A, mode, sms, st);
-        if (ng == 2) return launch_attention_t<128, 2>(A, mode, sms, st);
-        return launch_attention_t<128, 1>(A, mode, sms, st);
+        if (ng == 4) return launch_attention_t<128, 4>(A, mode, st);
+        if (ng == 2) return launch_attention_t<128, 2>(A, mode, st);
+        return launch_attention_t<128, 1>(A, mode, st);
     }
-    if (ng == 2) return launch_attention_t<64, 2>(A, mode, sms, st);
-    return launch_attention_t<64, 1>(A, mode, sms, st);
+    if (ng == 2) return launch_attention_t<64, 2>(A, mode, st);
+    return launch_attention_t<64, 1>(A, mode, st);
 }

@@ -382,39 +382,53 @@ def convert_fp8_e5m2(x16: np.ndarray) -> np.ndarray:
 # torch CUDA tensors in and out, enqueued on torch's current stream of their
 # device (or on `stream`, a torch.cuda.Stream).  Results are allocated by torch
 # where `out` is not given.
-DTYPES = {"float16": 0, "bfloat16": 1, "float32": 2}
+_torch = None
+DTYPES = {}      # torch dtype -> kie_dtype
+
+
+def _need_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        DTYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+        _torch = torch
+    return _torch
 
 
 def _dtype(t):
-    name = str(t.dtype).replace("torch.", "")
-    if name not in DTYPES:
-        raise ValueError(f"tensors must be float16, bfloat16 or float32, not {name}")
-    return DTYPES[name]
+    _need_torch()
+    d = DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"tensors must be float16, bfloat16 or float32, not {t.dtype}")
+    return d
 
 
 def _on(t, device, what):
-    if not getattr(t, "is_cuda", False) or t.device.index != device:
+    if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{what} must be a CUDA tensor on device {device}")
 
 
 def _vector(t, n, dtype, device, what):
-    """Address of a contiguous [n] tensor of `dtype` ("int32", "float32"); None stays None."""
+    """Address of a contiguous [n] tensor of `dtype`; None stays None."""
     if t is None:
         return None
     _on(t, device, what)
-    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape ({n},)")
     return t.data_ptr()
 
 
 def _rows(t, shape, device, what):
-    """(address, strides) of a 4-D tensor whose channels are contiguous."""
+    """(address, strides or None) of a 4-D tensor whose channels are contiguous."""
     _on(t, device, what)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.stride(3) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    s = t.stride()
+    if s[3] != 1:
         raise ValueError(f"{what} must have contiguous channels")
-    return t.data_ptr(), (C.c_int64 * 3)(*t.stride()[:3])
+    return t.data_ptr(), (C.c_int64 * 3)(*s[:3])
 
 
 def _written(t, what):
@@ -424,8 +438,7 @@ def _written(t, what):
 
 
 def _stream(stream, device):
-    import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return (_torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
 class KV4Cache:
@@ -434,7 +447,7 @@ class KV4Cache:
     per `group` channels.  Its memory is a torch tensor (`data`)."""
 
     def __init__(self, batch: int, n_kv_heads: int, max_ctx: int, head_dim: int, group: int = 32, device=None):
-        import torch
+        torch = _need_torch()
         device = torch.device("cuda" if device is None else device)
         index = torch.cuda.current_device() if device.index is None else device.index
         self.desc = kie_kv4_cache(None, batch, n_kv_heads, max_ctx, head_dim, group, index)
@@ -444,78 +457,78 @@ class KV4Cache:
                              f"head_dim {head_dim}, group {group}")
         self.data = torch.empty(n, dtype=torch.uint8, device=f"cuda:{index}")
         self.desc.data = self.data.data_ptr()
-
-    @property
-    def device(self) -> int:
-        return self.desc.device
-
-    def _shape(self, n):
-        return self.desc.batch, n, self.desc.n_kv_heads, self.desc.head_dim
+        self.batch, self.n_kv_heads, self.max_ctx, self.head_dim = batch, n_kv_heads, max_ctx, head_dim
+        self.group, self.device = group, index
+        self._ws_bytes = {}      # (tokens, heads, dtype) -> kie_kv4_attention_workspace
 
     def append(self, k, v, start, n_tok=None, stream=None):
         """kie_kv4_append: store k, v [batch, tokens, n_kv_heads, head_dim] (any
         strides with contiguous channels) at positions start[b] + t, t < n_tok[b]."""
-        d = self.desc
-        if k.dim() != 4 or k.dtype != v.dtype:
+        if k.dim() != 4 or k.dtype is not v.dtype:
             raise ValueError("k and v must be 4-D tensors of one type")
-        n = k.shape[1]
-        kp, ks = _rows(k, self._shape(n), d.device, "k")
-        vp, vs = _rows(v, self._shape(n), d.device, "v")
-        _check(load().kie_kv4_append(C.byref(d), kp, vp, _dtype(k), ks, vs, n,
-                                     _vector(start, d.batch, "int32", d.device, "start"),
-                                     _vector(n_tok, d.batch, "int32", d.device, "n_tok"), _stream(stream, d.device)))
+        b, n, dev = self.batch, k.shape[1], self.device
+        shape = (b, n, self.n_kv_heads, self.head_dim)
+        kp, ks = _rows(k, shape, dev, "k")
+        vp, vs = _rows(v, shape, dev, "v")
+        i32 = _torch.int32
+        _check(_lib.kie_kv4_append(self.desc, kp, vp, _dtype(k), ks, vs, n, _vector(start, b, i32, dev, "start"),
+                                   _vector(n_tok, b, i32, dev, "n_tok"), _stream(stream, dev)))
 
     def read(self, start, tokens: int, n_tok=None, out=None, dtype=None, stream=None):
         """kie_kv4_read: the values at positions start[b] + t, t < n_tok[b], as
         (k, v) [batch, tokens, n_kv_heads, head_dim]: `out`, or new tensors of
         `dtype` (float16) with zeros in the rows that are not read."""
-        import torch
-        d = self.desc
+        b, dev = self.batch, self.device
+        shape = (b, tokens, self.n_kv_heads, self.head_dim)
         if out is None:
-            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(d.device):
-                out = [torch.zeros(self._shape(tokens), dtype=dtype or torch.float16, device=self.data.device)
-                       for _ in range(2)]
+            with _torch.cuda.stream(stream):
+                out = [_torch.zeros(shape, dtype=dtype or _torch.float16, device=self.data.device) for _ in range(2)]
         k, v = out
-        if k.dtype != v.dtype:
+        if k.dtype is not v.dtype:
             raise ValueError("the two outputs must be of one type")
-        kp, ks = _rows(k, self._shape(tokens), d.device, "out[0]")
-        vp, vs = _rows(v, self._shape(tokens), d.device, "out[1]")
-        _written(k, "out[0]")
-        _written(v, "out[1]")
-        _check(load().kie_kv4_read(C.byref(d), kp, vp, _dtype(k), ks, vs, tokens,
-                                   _vector(start, d.batch, "int32", d.device, "start"),
-                                   _vector(n_tok, d.batch, "int32", d.device, "n_tok"), _stream(stream, d.device)))
+        kp, ks = _rows(k, shape, dev, "out[0]")
+        vp, vs = _rows(v, shape, dev, "out[1]")
+        if ks is not None:
+            _written(k, "out[0]")
+        if vs is not None:
+            _written(v, "out[1]")
+        i32 = _torch.int32
+        _check(_lib.kie_kv4_read(self.desc, kp, vp, _dtype(k), ks, vs, tokens, _vector(start, b, i32, dev, "start"),
+                                 _vector(n_tok, b, i32, dev, "n_tok"), _stream(stream, dev)))
         return k, v
 
     def attention(self, q, kv_len, n_tok=None, causal=True, window: int = 0, scale=None, out=None, stream=None):
         """kie_kv4_attention of q [batch, tokens, n_heads, head_dim] over the
         stored positions: `out`, or a new tensor like q with zeros in the rows
         from n_tok[b] on.  scale: 1/sqrt(head_dim) unless given."""
-        import torch
-        d = self.desc
+        if stream is not None:
+            # what is allocated here belongs to the stream that the kernels run on
+            with _torch.cuda.stream(stream):
+                return self.attention(q, kv_len, n_tok, causal, window, scale, out)
         if q.dim() != 4:
             raise ValueError("q must be a 4-D tensor")
+        b, dev = self.batch, self.device
         n, heads = q.shape[1], q.shape[2]
-        shape = (d.batch, n, heads, d.head_dim)
-        qp, qs = _rows(q, shape, d.device, "q")
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(d.device):
-            if out is None:
-                out = (torch.empty if n_tok is None else torch.zeros)(shape, dtype=q.dtype, device=q.device)
-            elif out.dtype != q.dtype:
-                raise ValueError("out must have q's type")
-            op, os_ = _rows(out, shape, d.device, "out")
+        shape = (b, n, heads, self.head_dim)
+        qp, qs = _rows(q, shape, dev, "q")
+        if out is None:
+            out = (_torch.empty if n_tok is None else _torch.zeros)(shape, dtype=q.dtype, device=q.device)
+        elif out.dtype is not q.dtype:
+            raise ValueError("out must have q's type")
+        op, os_ = _rows(out, shape, dev, "out")
+        if os_ is not None:
             _written(out, "out")
-            a = kie_kv4_query(qp, op, C.cast(qs, C.c_void_p), C.cast(os_, C.c_void_p),
-                              _vector(kv_len, d.batch, "int32", d.device, "kv_len"),
-                              _vector(n_tok, d.batch, "int32", d.device, "n_tok"), _dtype(q), n, heads,
-                              int(bool(causal)), int(window),
-                              float(d.head_dim ** -0.5 if scale is None else scale))
-            ws_bytes = load().kie_kv4_attention_workspace(C.byref(d), C.byref(a))
-            # of the stream that the kernels run on: the allocator gives it to no
-            # one else before they are done, and a graph keeps its own
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            _check(load().kie_kv4_attention(C.byref(d), C.byref(a), ws.data_ptr(), ws_bytes,
-                                            _stream(stream, d.device)))
+        dt, i32 = _dtype(q), _torch.int32
+        a = kie_kv4_query(qp, op, None if qs is None else C.addressof(qs), None if os_ is None else C.addressof(os_),
+                          _vector(kv_len, b, i32, dev, "kv_len"), _vector(n_tok, b, i32, dev, "n_tok"), dt, n, heads,
+                          bool(causal), window, self.head_dim ** -0.5 if scale is None else scale)
+        need = self._ws_bytes.get((n, heads, dt))
+        if need is None:
+            need = self._ws_bytes[n, heads, dt] = _lib.kie_kv4_attention_workspace(self.desc, a)
+        # of this call: the allocator gives it to no one else before the stream is
+        # done with it, and a captured graph keeps its own
+        ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
+        _check(_lib.kie_kv4_attention(self.desc, a, ws.data_ptr(), need, _stream(None, dev)))
         return out
 
 
@@ -523,23 +536,26 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     """kie_sample: a token per row of logits [rows, vocab] (contiguous within a
     row) from the random numbers u [rows], and its probability: (int32 [rows],
     fp32 [rows]), written to `tokens` and `probs` where given."""
-    import torch
+    torch = _need_torch()
+    load()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, tokens, probs)
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a 2-D CUDA tensor")
-    if logits.shape[1] > 1 and logits.stride(1) != 1:
-        raise ValueError("logits must be contiguous within a row")
     rows, vocab = logits.shape
-    dev = logits.device.index
-    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
-        if tokens is None:
-            tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
-        if probs is None:
-            probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        a = kie_sample_args(logits.data_ptr(), _dtype(logits), rows, vocab, logits.stride(0),
-                            _vector(temperature, rows, "float32", dev, "temperature"),
-                            _vector(top_k, rows, "int32", dev, "top_k"), _vector(top_p, rows, "float32", dev, "top_p"),
-                            _vector(min_p, rows, "float32", dev, "min_p"), _vector(u, rows, "float32", dev, "u"),
-                            _vector(tokens, rows, "int32", dev, "tokens"), _vector(probs, rows, "float32", dev, "probs"),
-                            dev)
-        _check(load().kie_sample(C.byref(a), _stream(stream, dev)))
+    stride, last = logits.stride()
+    if vocab > 1 and last != 1:
+        raise ValueError("logits must be contiguous within a row")
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=i32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(rows, dtype=f32, device=logits.device)
+    a = kie_sample_args(logits.data_ptr(), _dtype(logits), rows, vocab, stride,
+                        _vector(temperature, rows, f32, dev, "temperature"), _vector(top_k, rows, i32, dev, "top_k"),
+                        _vector(top_p, rows, f32, dev, "top_p"), _vector(min_p, rows, f32, dev, "min_p"),
+                        _vector(u, rows, f32, dev, "u"), _vector(tokens, rows, i32, dev, "tokens"),
+                        _vector(probs, rows, f32, dev, "probs"), dev)
+    _check(_lib.kie_sample(a, _stream(None, dev)))
     return tokens, probs

@@ -104,4 +104,4 @@ def test_python_checks():
     with pytest.raises(ValueError):
         kie._written(x[:1].expand(2, 8), "out")
     with pytest.raises(ValueError):
-        kie._vector(x, 2, "int32", 0, "start")
+        kie._vector(x, 2, torch.int32, 0, "start")
