@@ -1830,8 +1830,8 @@ kie_status kv4_rows(const kie_kv4_cache* c, const void* k, const void* v, int32_
     if (n_tokens > 0 && (!k || !v || !start || (reinterpret_cast<uintptr_t>(k) & mis) || (reinterpret_cast<uintptr_t>(v) & mis) ||
                          (reinterpret_cast<uintptr_t>(start) & 3u)))
         return fail(nullptr, KIE_ERR_INVALID_ARG, "NULL or misaligned pointer");
-    // 256 threads hold 16 or 32 rows: the grid stays below 2^31 blocks
-    if (int64_t(c->batch) * c->n_kv_heads * n_tokens > (int64_t(1) << 34)) return fail(nullptr, KIE_ERR_UNSUPPORTED, "too many rows");
+    // 32-bit row indices inside a request; a block holds at least 64 rows
+    if (int64_t(c->n_kv_heads) * n_tokens > (1 << 30) || int64_t(c->batch) * c->n_kv_heads * n_tokens > (int64_t(1) << 34)) return fail(nullptr, KIE_ERR_UNSUPPORTED, "too many rows");
     return KIE_OK;
 }
 

@@ -98,18 +98,6 @@ __device__ __forceinline__ void store8(typename Elem<T>::type* p, bool vec, cons
 
 __device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Where row `r` of [batch][n][head] rows goes: false when it is not stored.
-__device__ __forceinline__ bool place(const Kv4& c, int64_t r, int n, const int32_t* start, const int32_t* n_tok,
-                                      int& b, int& t, int& h, int64_t& pos) {
-    h = int(r % c.heads);
-    const int64_t bt = r / c.heads;
-    t = int(bt % n);
-    b = int(bt / n);
-    if (n_tok && t >= __ldg(n_tok + b)) return false;
-    pos = int64_t(__ldg(start + b)) + t;
-    return pos >= 0 && pos < c.max_ctx;
-}
-
 // Where the scale and the zero of a row's group lie, in fp16 elements of the params
 // (rows of a head start at multiples of 64, so a row's place in its block is row % 8).
 struct ParAt { size_t s, z; };
@@ -120,109 +108,168 @@ __device__ __forceinline__ ParAt par_at(size_t row, int gi, int ng, bool isv) {
     return ParAt{row * (2 * ng) + gi, row * (2 * ng) + ng + gi};
 }
 
-// ---- store -------------------------------------------------------------------------------------
-// A row (one position of one head, K or V) is D/8 lanes with 8 channels each.
-template <int T, int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(Kv4 c, const void* k, const void* v, Kv4Strides ks,
-                                                         Kv4Strides vs, int n, const int32_t* start,
-                                                         const int32_t* n_tok) {
-    using E = typename Elem<T>::type;
-    constexpr int LPR = D / 8, BLK = D / 32;
-    const int lane = threadIdx.x & 31, l = lane % LPR;
-    const int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR;
-    const bool isv = blockIdx.y != 0;
-    int b = 0, t = 0, h = 0;
-    int64_t pos = 0;
-    const bool ok = r < int64_t(c.batch) * n * c.heads && place(c, r, n, start, n_tok, b, t, h, pos);
-    const Kv4Strides& s = isv ? vs : ks;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (ok) {
-        const E* p = static_cast<const E*>(isv ? v : k) + b * s.b + t * s.t + h * s.h + l * 8;
-        load8<T>(p, aligned16(p), x);
-    }
-    // to fp16, saturating; the format has no NaN: stored as 0
-    float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float y = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -65504.f), 65504.f);
-        x[i] = __half2float(__float2half_rn(y));
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-    }
-    for (int o = 1; o < c.group / 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
-    const float sf = __half2float(sh);
-    const float rcp = sf > 0.f ? __frcp_rn(sf) : 0.f;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // (x - z) / s by the reciprocal: within 2^-19 of the quotient, so only a
-        // value that close to a half needs the division itself
-        const float d = x[i] - lo;
-        float q = d * rcp;
-        const float f = q - floorf(q);
-        if (fabsf(f - 0.5f) < 1.f / 65536.f) q = sf > 0.f ? __fdiv_rn(d, sf) : 0.f;
-        w |= uint32_t(min(15, int(rintf(q)))) << (4 * i);
-    }
-    const size_t row = (size_t(b) * c.heads + h) * c.ctx_pad + size_t(pos);
-    if (!isv) {
-        if (ok) reinterpret_cast<uint32_t*>(c.kc)[row * LPR + (l & 3) * BLK + (l >> 2)] = w;
+// ---- store and read back -----------------------------------------------------------------------
+// A row (one position of one head, K or V) is D/8 lanes of 8 channels.  A block
+// takes RB consecutive rows [token][head] of one request, RPT of them per lane
+// group, so that a thread has RPT independent loads in flight.
+constexpr int RPT = 4;
+template <int D> __host__ __device__ constexpr int rows_per_block() { return 256 / (D / 8) * RPT; }
+
+struct RowArgs {
+    Kv4 c;
+    Kv4Strides ks, vs;
+    const int32_t *start, *n_tok;
+    int32_t n, chunks;       // tokens, blocks per request
+};
+
+// This thread's k-th row: its token and head, and where it is stored (false: nowhere).
+struct Place { int b, t, h; size_t row; };
+template <int D>
+__device__ __forceinline__ bool place(const RowArgs& A, int k, Place& p) {
+    p.b = int(blockIdx.x) / A.chunks;
+    const int first = (int(blockIdx.x) - p.b * A.chunks) * rows_per_block<D>();
+    const int r = first + k * (256 / (D / 8)) + threadIdx.x / (D / 8);
+    p.t = r / A.c.heads;
+    p.h = r - p.t * A.c.heads;
+    const int nt = A.n_tok ? min(__ldg(A.n_tok + p.b), A.n) : A.n;
+    const int64_t pos = int64_t(__ldg(A.start + p.b)) + p.t;
+    p.row = (size_t(p.b) * A.c.heads + p.h) * A.c.ctx_pad + size_t(pos);
+    return p.t < nt && pos >= 0 && pos < A.c.max_ctx;
+}
+
+// Eight channels as fp16 pairs, saturated to +-65504, NaN as 0.
+template <int T>
+__device__ __forceinline__ void load_h2(const typename Elem<T>::type* p, __half2* x) {
+    if (T == KV4_F16 && aligned16(p)) {
+        *reinterpret_cast<uint4*>(x) = __ldg(reinterpret_cast<const uint4*>(p));
     } else {
-        // lane l stores word l = units (g, 2wi) and (g, 2wi + 1): see kie_kv4.h
-        const int g = l / (D / 64), wi = l % (D / 64);
-        const int src = (lane - l) + 8 * wi + (g >> 1);
-        const uint32_t w0 = __shfl_sync(0xffffffffu, w, src), w1 = __shfl_sync(0xffffffffu, w, src + 4);
-        const uint32_t out = __byte_perm(w0, w1, (g & 1) ? 0x7632 : 0x5410);
-        if (ok) reinterpret_cast<uint32_t*>(c.vc)[row * LPR + l] = out;
-    }
-    const int ng = D / c.group, lpg = c.group / 8;
-    if (ok && l % lpg == 0) {
-        const ParAt at = par_at(row, l / lpg, ng, isv);
-        uint16_t* pp = isv ? c.vp : c.kp;
-        pp[at.s] = __half_as_ushort(sh);
-        pp[at.z] = __half_as_ushort(__float2half_rn(lo));
+        float f[8];
+        load8<T>(p, aligned16(p), f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
     }
 }
 
-// ---- read back ---------------------------------------------------------------------------------
 template <int T, int D>
-__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4 c, void* k, void* v, Kv4Strides ks, Kv4Strides vs, int n,
-                                                       const int32_t* start, const int32_t* n_tok) {
+__global__ void __launch_bounds__(256) kv4_append_kernel(const RowArgs A, const void* k, const void* v) {
+    using E = typename Elem<T>::type;
+    constexpr int LPR = D / 8, BLK = D / 32;
+    const int lane = threadIdx.x & 31, l = lane % LPR;
+    const bool isv = blockIdx.y != 0;
+    const Kv4& c = A.c;
+    const Kv4Strides& s = isv ? A.vs : A.ks;
+    const int ng = D / c.group, lpg = c.group / 8;
+    Place p[RPT];
+    bool ok[RPT];
+    __half2 x[RPT][4];
+#pragma unroll
+    for (int u = 0; u < RPT; ++u) {
+        ok[u] = place<D>(A, u, p[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[u][i] = __half2half2(__ushort_as_half(0));
+        if (ok[u]) load_h2<T>(static_cast<const E*>(isv ? v : k) + p[u].b * s.b + p[u].t * s.t + p[u].h * s.h + l * 8, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < RPT; ++u) {
+        if (!__any_sync(0xffffffffu, ok[u])) continue;
+        const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), bottom = __hneg2(top);
+        __half2 lo2 = top, hi2 = bottom;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t num = __heq2_mask(x[u][i], x[u][i]);           // 0 where NaN
+            uint32_t w = *reinterpret_cast<uint32_t*>(&x[u][i]) & num;
+            x[u][i] = __hmax2(__hmin2(*reinterpret_cast<__half2*>(&w), top), bottom);
+            lo2 = __hmin2(lo2, x[u][i]);
+            hi2 = __hmax2(hi2, x[u][i]);
+        }
+        // (minimum, -maximum) of the lane, then of the group: one exchange per step
+        __half2 mm = __halves2half2(__hmin(__low2half(lo2), __high2half(lo2)), __hneg(__hmax(__low2half(hi2), __high2half(hi2))));
+        for (int o = 1; o < lpg; o <<= 1) mm = __hmin2(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        const float lo = __low2float(mm), hi = -__high2float(mm);
+        const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+        const float sf = __half2float(sh);
+        const float rcp = sf > 0.f ? __frcp_rn(sf) : 0.f;
+        // code = rint((x - z) / s), at most 15: by the reciprocal, which is within 2^-19 of
+        // the quotient, so only a value that close to a half needs the division itself.
+        // Adding 1.5 * 2^23 rounds to even and leaves the code in the low bits.
+        constexpr float MAGIC = 12582912.f;
+        float d[8], c8[8];
+        bool close = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            d[i] = (i & 1 ? __high2float(x[u][i >> 1]) : __low2float(x[u][i >> 1])) - lo;
+            const float q = d[i] * rcp;
+            c8[i] = q + MAGIC;
+            close |= fabsf(q - (c8[i] - MAGIC)) > 0.5f - 1.f / 65536.f;
+        }
+        if (close && sf > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c8[i] = rintf(__fdiv_rn(d[i], sf)) + MAGIC;
+        }
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) w = w * 16u + (__float_as_uint(fminf(c8[i], MAGIC + 15.f)) & 15u);
+        if (!isv) {
+            if (ok[u]) reinterpret_cast<uint32_t*>(c.kc)[p[u].row * LPR + (l & 3) * BLK + (l >> 2)] = w;
+        } else {
+            // lane l stores word l = units (g, 2wi) and (g, 2wi + 1): see kie_kv4.h
+            const int g = l / (D / 64), wi = l % (D / 64);
+            const int src = (lane - l) + 8 * wi + (g >> 1);
+            const uint32_t w0 = __shfl_sync(0xffffffffu, w, src), w1 = __shfl_sync(0xffffffffu, w, src + 4);
+            if (ok[u]) reinterpret_cast<uint32_t*>(c.vc)[p[u].row * LPR + l] = __byte_perm(w0, w1, (g & 1) ? 0x7632 : 0x5410);
+        }
+        if (ok[u] && l % lpg == 0) {
+            const ParAt at = par_at(p[u].row, l / lpg, ng, isv);
+            uint16_t* pp = isv ? c.vp : c.kp;
+            pp[at.s] = __half_as_ushort(sh);
+            pp[at.z] = __half_as_ushort(__low2half(mm));
+        }
+    }
+}
+
+template <int T, int D>
+__global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k, void* v) {
     using E = typename Elem<T>::type;
     constexpr int LPR = D / 8, BLK = D / 32;
     const int l = threadIdx.x % LPR;
-    const int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR;
     const bool isv = blockIdx.y != 0;
-    if (r >= int64_t(c.batch) * n * c.heads) return;
-    int b, t, h;
-    int64_t pos;
-    if (!place(c, r, n, start, n_tok, b, t, h, pos)) return;
-    const size_t row = (size_t(b) * c.heads + h) * c.ctx_pad + size_t(pos);
-    uint32_t w;
-    if (!isv) {
-        w = reinterpret_cast<const uint32_t*>(c.kc)[row * LPR + (l & 3) * BLK + (l >> 2)];
-    } else {
-        const uint16_t* u = reinterpret_cast<const uint16_t*>(c.vc) + row * (D / 4) + (2 * (l & 3)) * BLK + (l >> 2);
-        w = uint32_t(u[0]) | uint32_t(u[BLK]) << 16;
-    }
+    const Kv4& c = A.c;
+    const Kv4Strides& st = isv ? A.vs : A.ks;
     const int ng = D / c.group, gi = l * 8 / c.group;
-    const ParAt at = par_at(row, gi, ng, isv);
-    const uint16_t* pp = isv ? c.vp : c.kp;
-    const float s = __half2float(__ushort_as_half(pp[at.s])), z = __half2float(__ushort_as_half(pp[at.z]));
-    float f[8];
+    Place p[RPT];
+    bool ok[RPT];
+    uint32_t w[RPT];
+    uint16_t sz[RPT][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[i] = fmaf(float((w >> (4 * i)) & 15u), s, z);
-        if (T == KV4_F16) f[i] = fminf(fmaxf(f[i], -65504.f), 65504.f);
+    for (int u = 0; u < RPT; ++u) {
+        ok[u] = place<D>(A, u, p[u]);
+        if (!ok[u]) continue;
+        const size_t row = p[u].row;
+        if (!isv) {
+            w[u] = __ldg(reinterpret_cast<const uint32_t*>(c.kc) + row * LPR + (l & 3) * BLK + (l >> 2));
+        } else {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(c.vc) + row * (D / 4) + (2 * (l & 3)) * BLK + (l >> 2);
+            w[u] = uint32_t(__ldg(q)) | uint32_t(__ldg(q + BLK)) << 16;
+        }
+        const ParAt at = par_at(row, gi, ng, isv);
+        const uint16_t* pp = isv ? c.vp : c.kp;
+        sz[u][0] = __ldg(pp + at.s);
+        sz[u][1] = __ldg(pp + at.z);
     }
-    const Kv4Strides& st = isv ? vs : ks;
-    E* p = static_cast<E*>(isv ? v : k) + b * st.b + t * st.t + h * st.h + l * 8;
-    store8<T>(p, aligned16(p), f);
+#pragma unroll
+    for (int u = 0; u < RPT; ++u) {
+        if (!ok[u]) continue;
+        const float s = __half2float(__ushort_as_half(sz[u][0])), z = __half2float(__ushort_as_half(sz[u][1]));
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float code = __uint_as_float(((w[u] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f;
+            f[i] = fmaf(code, s, z);
+            if (T == KV4_F16) f[i] = fminf(fmaxf(f[i], -65504.f), 65504.f);
+        }
+        E* q = static_cast<E*>(isv ? v : k) + p[u].b * st.b + p[u].t * st.t + p[u].h * st.h + l * 8;
+        store8<T>(q, aligned16(q), f);
+    }
 }
 
 // ---- attention ---------------------------------------------------------------------------------
@@ -1095,22 +1142,19 @@ cudaError_t launch_attention_t(const AttnArgs& A, int mode, cudaStream_t st) {
     return mode == S8 ? launch_attention<D, NG, S8, KV4_BF16>(A, st) : launch_attention<D, NG, S16, KV4_BF16>(A, st);
 }
 
-template <int T>
-cudaError_t append_t(const Kv4& c, const void* k, const void* v, const Kv4Strides& ks, const Kv4Strides& vs, int n,
-                     const int32_t* start, const int32_t* n_tok, cudaStream_t st) {
-    const int64_t threads = int64_t(c.batch) * n * c.heads * (c.dim / 8);
-    const dim3 grid(unsigned((threads + 255) / 256), 2);
-    if (c.dim == 128) kv4_append_kernel<T, 128><<<grid, 256, 0, st>>>(c, k, v, ks, vs, n, start, n_tok);
-    else kv4_append_kernel<T, 64><<<grid, 256, 0, st>>>(c, k, v, ks, vs, n, start, n_tok);
+template <int D>
+RowArgs row_args(const Kv4& c, const Kv4Strides& ks, const Kv4Strides& vs, int n, const int32_t* start,
+                 const int32_t* n_tok) {
+    return RowArgs{c, ks, vs, start, n_tok, n, int((int64_t(n) * c.heads + rows_per_block<D>() - 1) / rows_per_block<D>())};
+}
+template <int T, int D>
+cudaError_t append_t(const RowArgs& A, const void* k, const void* v, cudaStream_t st) {
+    kv4_append_kernel<T, D><<<dim3(unsigned(A.chunks) * A.c.batch, 2), 256, 0, st>>>(A, k, v);
     return cudaGetLastError();
 }
-template <int T>
-cudaError_t read_t(const Kv4& c, void* k, void* v, const Kv4Strides& ks, const Kv4Strides& vs, int n,
-                   const int32_t* start, const int32_t* n_tok, cudaStream_t st) {
-    const int64_t threads = int64_t(c.batch) * n * c.heads * (c.dim / 8);
-    const dim3 grid(unsigned((threads + 255) / 256), 2);
-    if (c.dim == 128) kv4_read_kernel<T, 128><<<grid, 256, 0, st>>>(c, k, v, ks, vs, n, start, n_tok);
-    else kv4_read_kernel<T, 64><<<grid, 256, 0, st>>>(c, k, v, ks, vs, n, start, n_tok);
+template <int T, int D>
+cudaError_t read_t(const RowArgs& A, void* k, void* v, cudaStream_t st) {
+    kv4_read_kernel<T, D><<<dim3(unsigned(A.chunks) * A.c.batch, 2), 256, 0, st>>>(A, k, v);
     return cudaGetLastError();
 }
 
@@ -1119,17 +1163,27 @@ cudaError_t read_t(const Kv4& c, void* k, void* v, const Kv4Strides& ks, const K
 extern "C" cudaError_t kie_launch_kv4_append(const Kv4* c, const void* k, const void* v, const Kv4Strides* ks,
                                              const Kv4Strides* vs, int type, int n, const int32_t* start,
                                              const int32_t* n_tok, cudaStream_t st) {
-    if (type == KV4_F16) return append_t<KV4_F16>(*c, k, v, *ks, *vs, n, start, n_tok, st);
-    if (type == KV4_BF16) return append_t<KV4_BF16>(*c, k, v, *ks, *vs, n, start, n_tok, st);
-    return append_t<KV4_F32>(*c, k, v, *ks, *vs, n, start, n_tok, st);
+    if (c->dim == 128) {
+        const RowArgs A = row_args<128>(*c, *ks, *vs, n, start, n_tok);
+        return type == KV4_F16 ? append_t<KV4_F16, 128>(A, k, v, st) : type == KV4_BF16 ? append_t<KV4_BF16, 128>(A, k, v, st)
+                                                                                       : append_t<KV4_F32, 128>(A, k, v, st);
+    }
+    const RowArgs A = row_args<64>(*c, *ks, *vs, n, start, n_tok);
+    return type == KV4_F16 ? append_t<KV4_F16, 64>(A, k, v, st) : type == KV4_BF16 ? append_t<KV4_BF16, 64>(A, k, v, st)
+                                                                                  : append_t<KV4_F32, 64>(A, k, v, st);
 }
 
 extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const Kv4Strides* ks, const Kv4Strides* vs,
                                            int type, int n, const int32_t* start, const int32_t* n_tok,
                                            cudaStream_t st) {
-    if (type == KV4_F16) return read_t<KV4_F16>(*c, k, v, *ks, *vs, n, start, n_tok, st);
-    if (type == KV4_BF16) return read_t<KV4_BF16>(*c, k, v, *ks, *vs, n, start, n_tok, st);
-    return read_t<KV4_F32>(*c, k, v, *ks, *vs, n, start, n_tok, st);
+    if (c->dim == 128) {
+        const RowArgs A = row_args<128>(*c, *ks, *vs, n, start, n_tok);
+        return type == KV4_F16 ? read_t<KV4_F16, 128>(A, k, v, st) : type == KV4_BF16 ? read_t<KV4_BF16, 128>(A, k, v, st)
+                                                                                     : read_t<KV4_F32, 128>(A, k, v, st);
+    }
+    const RowArgs A = row_args<64>(*c, *ks, *vs, n, start, n_tok);
+    return type == KV4_F16 ? read_t<KV4_F16, 64>(A, k, v, st) : type == KV4_BF16 ? read_t<KV4_BF16, 64>(A, k, v, st)
+                                                                                : read_t<KV4_F32, 64>(A, k, v, st);
 }
 
 // A partial of CTA i for item k lies at slot k + i: a CTA's items and an item's

@@ -15,15 +15,20 @@
 // from the definition's only where u falls within about 2^-37 of a border.
 //
 // One cluster per row, the row's logits read once into its CTAs' shared memory.
-// The prefix's end is found by a histogram over y = (m - l) log2(e) / T in steps
-// of 1/16 (counts and masses), a second one inside the bin that holds the end,
-// and then among the few tokens left (or, for crowds of near-equal logits, by
-// further histograms over the bits of the logit).  No sort.
+// y = (m - l) log2(e) / T puts the logits into bins of 1/16.  No sort of the row:
+//   a small top-k: the counts of the bins say which hold the first k; their few
+//     tokens go to one CTA, which sorts them and applies every filter there;
+//   top-p alone: masses of 14 bits per token and bin say in which bin or two the
+//     prefix must end; one pass of exact weights then needs the histogram for
+//     those alone, and plain sums for what lies before and after;
+//   the end of the prefix inside its bin: histograms over the bits of the logit, a
+//     thousand steps each, until one value or a few tokens are left.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kie_device.cuh"
 #include "kie_sample.h"
@@ -37,8 +42,9 @@ constexpr int NB = 1024;                   // histogram bins (two per thread)
 constexpr int FRAC = 44;                   // masses count 2^-44
 constexpr int LIST = 32;                   // candidates resolved by one warp
 constexpr int MAXC = 8;                    // CTAs per row
+constexpr int KLIM = 512, CAP = 1024;      // the sorted path: largest top-k, most candidates
 
-// 2^(-j/128) * 2^63, by the series of exp(-j ln 2 / 128) (to 2^-52)
+// 2^(-j/128) * 2^60, by the series of exp(-j ln 2 / 128) (to 2^-52)
 struct Pow2 { uint64_t v[128]; };
 constexpr Pow2 make_pow2() {
     Pow2 t{};
@@ -46,7 +52,7 @@ constexpr Pow2 make_pow2() {
         const double a = -0.693147180559945309417 * j / 128.0;
         double s = 0.0;
         for (int k = 24; k >= 1; --k) s = (1.0 + s) * a / k;   // a + a^2/2! + ...
-        t.v[j] = uint64_t((1.0 + s) * 9223372036854775808.0);
+        t.v[j] = uint64_t((1.0 + s) * 1152921504606846976.0);
     }
     return t;
 }
@@ -55,8 +61,8 @@ __device__ constexpr Pow2 kPow2 = make_pow2();
 struct Shared {
     uint32_t h[4][NB];          // local histogram: counts, three 15-bit limbs of the masses
     uint32_t fc[2][NB];         // this CTA's share of the summed histogram: counts, masses
-    uint64_t fm[2][NB];
-    uint64_t table[128];        // 2^(-j/128) * 2^63
+    uint64_t fm[2][NB];         // sorted path: masses, sort keys
+    uint64_t table[128];        // 2^(-j/128) * 2^60
     uint64_t xch[4][4];         // values other CTAs read, by exchange number
     uint64_t list_w[LIST];
     uint32_t list_key[LIST];
@@ -82,12 +88,21 @@ template <> __device__ __forceinline__ float to_float<0>(const void* p, int64_t 
 template <> __device__ __forceinline__ float to_float<1>(const void* p, int64_t i) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]); }
 template <> __device__ __forceinline__ float to_float<2>(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
 
-// Order-preserving integer of a float (-0 and 0 are one value).
+// Order-preserving integer of a logit (-0 and 0 are one value): of its own 16 bits
+// where the type has no more, so that neighbours differ by one.
+template <int T>
 __device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x + 0.f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    if (T == 0) {
+        const uint32_t b = __half_as_ushort(__float2half_rn(x + 0.f));
+        return b & 0x8000u ? 0xFFFFu & ~b : b | 0x8000u;
+    }
+    const uint32_t b = __float_as_uint(x + 0.f), k = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return T == 1 ? k >> 16 : k;
 }
+template <int T>
 __device__ __forceinline__ float of_key(uint32_t k) {
+    if (T == 0) return __half2float(__ushort_as_half(uint16_t(k & 0x8000u ? k & 0x7FFFu : ~k)));
+    if (T == 1) return __uint_as_float((k & 0x8000u ? k & 0x7FFFu : 0xFFFFu & ~k) << 16);
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
@@ -97,30 +112,36 @@ struct Row {
     const uint64_t* table;
     // (m - l) log2(e) / T in fp32: monotone in l
     __device__ __forceinline__ float y(float l) const { return (m - l) * chi; }
-    // exp((l - m) / T) in units of 2^-44, to about 2^-43 relative
+    // exp((l - m) / T) in units of 2^-44, to about 2^-39 relative.  Floats become
+    // integers by adding 1.5 * 2^23 and reading the bits: conversions run at an
+    // eighth of the additions' rate.
     __device__ __forceinline__ uint64_t weight(float l) const {
+        constexpr float MAGIC = 12582912.f;
+        constexpr int MAGIC_BITS = 0x4B400000;
         const float hi = m - l;
-        const float yh = hi * chi;
-        if (!(yh < 46.f)) return 0;                        // below half a unit (l = -inf too)
         const float bb = hi - m, lo = (m - (hi - bb)) - (l + bb);   // m - l = hi + lo exactly
+        const float yh = hi * chi;
         const float yl = fmaf(hi, clo, fmaf(lo, chi, fmaf(hi, chi, -yh)));
         // y = k / 128 + f + yl, |f| <= 1/256, f exact
-        const float kf = rintf(yh * 128.f);
-        const float f = fmaf(kf, -1.f / 128.f, yh);
-        const int k = int(kf);
+        const float kr = fmaf(yh, 128.f, MAGIC);
+        const float f = fmaf(kr - MAGIC, -1.f / 128.f, yh);
+        const int k = __float_as_int(kr) - MAGIC_BITS;
         // 2^-(f + yl) = 1 - a + a^2/2 - ..., a = (f + yl) ln 2 = ah + al
         constexpr float L1 = 0.693147182464599609375f, L2 = -1.904654299957767e-9f;   // ln 2 = L1 + L2
         const float ah = f * L1;
         const float al = fmaf(yl, L1, fmaf(f, L2, fmaf(f, L1, -ah)));
-        const float q = fmaf(ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al * fmaf(al, 0.5f, ah));
-        // to units of 2^-48: the large term in two exact steps, the small ones (below 2^-17) in one
-        const float a1 = rintf(ah * 1048576.f);                     // 2^20
-        const float a2 = fmaf(ah, 1048576.f, -a1) * 268435456.f;    // the rest, 2^48
-        const int64_t F = (int64_t(1) << 48) - (int64_t(int(a1)) << 28) - int64_t(__float2int_rn(a2)) +
-                          int64_t(__float2int_rn((q - al) * 70368744177664.f)) * 4;
-        const uint64_t p = __umul64hi(uint64_t(F) << 14, table[k & 127]);   // 2^(62 + 63 - 64) = 2^61
-        const int sh = 61 - FRAC + (k >> 7);
-        return sh >= 64 ? 0 : (p + (uint64_t(1) << (sh - 1))) >> sh;
+        const float q = fmaf(ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al * fmaf(al, 0.5f, fmaf(ah * ah, -0.5f, ah)));
+        // that minus 1 in units of 2^-39: a's large part in two exact steps, the rest (below 2^-17) in one
+        const float r1 = fmaf(ah, 1048576.f, MAGIC);                              // 2^20
+        const float r2 = fmaf(fmaf(ah, 1048576.f, -(r1 - MAGIC)), 524288.f, MAGIC);   // 2^19 more
+        const float r3 = fmaf(q - al, 549755813888.f, MAGIC);                     // 2^39
+        const int G = (__float_as_int(r3) - MAGIC_BITS) - (__float_as_int(r2) - MAGIC_BITS) -
+                      ((__float_as_int(r1) - MAGIC_BITS) << 19);
+        const uint64_t V = table[k & 127];
+        const uint64_t p = V + uint64_t((int64_t(int(V >> 30)) * G) >> 9);        // units of 2^-60
+        const int sh = 60 - FRAC + (k >> 7);
+        const uint64_t w = (p + (1ull << (sh - 1))) >> (sh & 63);
+        return yh < 46.f ? w : 0;                          // below half a unit (l = -inf too)
     }
 };
 
@@ -130,10 +151,10 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
     return v;
 }
 
-__device__ __forceinline__ int bin_of(float y) { return y < float(NB - 1) / 16.f ? int(y * 16.f) : NB - 1; }
-__device__ __forceinline__ int sub_of(float y, int b) {
-    const float f = (fminf(y, 1.0e9f) * 16.f - float(b)) * float(NB);
-    return f < float(NB - 1) ? int(f) : NB - 1;
+// Bin of y: its sixteenths, rounded down (the addition of 2^23 does that), the last
+// bin for all from 1023 / 16 on (and for NaN, an infinite distance at an infinite T).
+__device__ __forceinline__ int bin_of(float y) {
+    return __float_as_int(__fadd_rd(fminf(y * 16.f, float(NB - 1)), 8388608.f)) - 0x4B000000;
 }
 
 template <int T>
@@ -152,7 +173,30 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     float mx = -INFINITY;
     {
         const int64_t base = int64_t(row) * A.row_stride + s0;
-        for (int i = tid; i < n; i += NT) {
+        constexpr int W = T == 2 ? 4 : 8;          // elements of 16 bytes
+        const uint8_t* src = static_cast<const uint8_t*>(A.logits) + base * (16 / W);
+        const int nv = (reinterpret_cast<uintptr_t>(src) & 15u) ? 0 : n / W;
+        auto put = [&](int i, const uint4& w) {
+            float v[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                v[j] = to_float<T>(&w, j);
+                if (v[j] != v[j]) v[j] = -INFINITY;
+                mx = fmaxf(mx, v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < W; j += 4) *reinterpret_cast<float4*>(x + i * W + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        };
+        int i = tid;
+        for (; i + 3 * NT < nv; i += 4 * NT) {      // four loads in flight
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(src) + i + j * NT);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) put(i + j * NT, w[j]);
+        }
+        for (; i < nv; i += NT) put(i, __ldg(reinterpret_cast<const uint4*>(src) + i));
+        for (int i = nv * W + tid; i < n; i += NT) {
             float v = to_float<T>(A.logits, base + i);
             if (v != v) v = -INFINITY;
             x[i] = v;
@@ -216,29 +260,83 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     }
     const Row R{mx, sh.chi, sh.clo, sh.table};
 
+    // Sum over the CTA's threads, for all of them; exclusive prefix and total of it.
+    auto block_sum = [&](uint64_t v) {
+        v = warp_sum64(v);
+        __syncthreads();
+        if (lane == 0) sh.wsum[warp] = v;
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int w = 0; w < NWARP; ++w) v += sh.wsum[w];
+        return v;
+    };
+    auto block_prefix = [&](uint64_t v, uint64_t& total) {
+        uint64_t inc = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.wsum[warp] = inc;
+        __syncthreads();
+        uint64_t before = inc - v;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < NWARP; ++w) {
+            before += w < warp ? sh.wsum[w] : 0ull;
+            total += sh.wsum[w];
+        }
+        return before;
+    };
+
     const int top_k = A.top_k ? A.top_k[row] : 0;
     const float top_p = A.top_p ? A.top_p[row] : 1.f;
     const bool use_k = top_k > 0 && top_k < A.vocab, use_p = top_p < 1.f;
 
+    constexpr int ABOVE = -2, BELOW = -3;
     // Histogram of the elements for which binf gives a bin (>= 0), summed over the
-    // cluster: afterwards each CTA holds its share of the sums in fc/fm[which].
-    auto histogram = [&](int which, auto binf) {
+    // cluster: afterwards each CTA holds its share of the sums in fc/fm[which] and,
+    // where `sums` asks for it, the masses of what binf calls ABOVE and BELOW are in
+    // above and below.
+    uint64_t above = 0, below = 0;
+    auto histogram = [&](int which, auto binf, auto sums) {
         for (int i = tid; i < 4 * NB; i += NT) (&sh.h[0][0])[i] = 0u;
         __syncthreads();
+        uint64_t sa = 0, sb = 0;
         for (int i = tid; i < n; i += NT) {
             const float l = x[i];
             const int b = binf(l);
-            if (b >= 0) {
-                atomicAdd(&sh.h[0][b], 1u);
+            if (b >= 0 || (sums.value && b != -1)) {
                 const uint64_t w = R.weight(l);
-                if (w) {
+                if (b < 0) {
+                    sa += b == ABOVE ? w : 0ull;
+                    sb += b == ABOVE ? 0ull : w;
+                } else {
+                    atomicAdd(&sh.h[0][b], 1u);
+                }
+                if (w && b >= 0) {
                     atomicAdd(&sh.h[1][b], uint32_t(w) & 0x7FFFu);
                     atomicAdd(&sh.h[2][b], uint32_t(w >> 15) & 0x7FFFu);
                     atomicAdd(&sh.h[3][b], uint32_t(w >> 30));
                 }
             }
         }
+        if (sums.value) {
+            sa = block_sum(sa);
+            sb = block_sum(sb);
+            if (tid == 0) { sh.xch[ex][0] = sa; sh.xch[ex][1] = sb; }
+        }
         sync();
+        if (sums.value) {
+            above = below = 0;
+            for (int r = 0; r < C; ++r) {
+                above += cl.map_shared_rank(&sh, r)->xch[ex][0];
+                below += cl.map_shared_rank(&sh, r)->xch[ex][1];
+            }
+            ex = (ex + 1) & 3;
+        }
         const int per = NB / C;
         for (int i = tid; i < per; i += NT) {
             const int b = rank * per + i;
@@ -293,25 +391,55 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     };
     // The shortest prefix whose count (mass) reaches target: it ends with the
     // n_eq lowest-indexed of the all_eq tokens of logit of_key(key).
-    auto select = [&](bool by_mass, uint64_t target) {
-        find(0, by_mass, target, 0u, 0ull);
+    auto select = [&](bool by_mass, uint64_t target, uint64_t mass0) {   // mass0: before the first histogram
+        find(0, by_mass, target, 0u, mass0);
         const int b = sh.f_bin;
         uint32_t cnt = sh.f_cnt;
         uint64_t mass = sh.f_mass;
-        histogram(1, [&](float l) { const float y = R.y(l); return bin_of(y) == b ? sub_of(y, b) : -1; });
-        find(1, by_mass, target, cnt, mass);
-        const int s = sh.f_bin;
-        cnt = sh.f_cnt;
-        mass = sh.f_mass;
-        const uint32_t nc = sh.f_n;
-        auto here = [&](float l) { const float y = R.y(l); return bin_of(y) == b && sub_of(y, b) == s; };
-        if (nc <= LIST) {
+        // the keys that the bin can hold: its ends in logits, a hundredth of a bin and
+        // two neighbours wider than the rounding of y and of the ends can reach
+        const float wide = 1.f / (16.f * R.chi);
+        uint32_t hi = key_of<T>(R.m - (float(b) - 0.01f) * wide), lo = b == NB - 1 ? 0u : key_of<T>(R.m - (float(b) + 1.01f) * wide);
+        hi = min(hi, key_of<T>(R.m) - 2u) + 2u;
+        lo = max(lo, 2u) - 2u;
+        for (int level = 0; level < 4; ++level) {    // 2^32 -> 2^22 -> 2^12 -> 2^2 -> 1 keys
+            int shift = 0;
+            while (shift < 22 && ((hi - lo) >> shift) >= NB) ++shift;
+            auto here = [&](float l) {
+                const uint32_t k = key_of<T>(l);
+                if (level == 0 ? bin_of(R.y(l)) != b : k < lo || k > hi) return -1;
+                return int(min((hi - min(k, hi)) >> shift, uint32_t(NB - 1)));
+            };
+            histogram(1, here, std::false_type());
+            find(1, by_mass, target, cnt, mass);
+            const int s = sh.f_bin;
+            const uint32_t nc = sh.f_n;
+            cnt = sh.f_cnt;
+            mass = sh.f_mass;
+            if (shift == 0) {
+                if (tid == 0) {
+                    hi -= uint32_t(s);
+                    const uint64_t w = R.weight(of_key<T>(hi));
+                    const uint64_t need = by_mass ? (w ? (target - mass + w - 1) / w : nc) : target - cnt;
+                    sh.key = hi;
+                    sh.all_eq = nc;
+                    sh.n_eq = uint32_t(need < nc ? need : nc);
+                    sh.mass = mass + sh.n_eq * w;
+                }
+                __syncthreads();
+                return;
+            }
+            if (nc > LIST) {           // many near-equal logits: into the bucket's keys
+                hi -= uint32_t(s) << shift;
+                lo = max(lo, hi - ((1u << shift) - 1u));
+                continue;
+            }
             if (tid == 0) sh.list_n = 0;
             __syncthreads();
             for (int i = tid; i < n; i += NT)
-                if (here(x[i])) {
+                if (here(x[i]) == s) {
                     const uint32_t at = atomicAdd(&sh.list_n, 1u);
-                    sh.list_key[at] = key_of(x[i]);
+                    sh.list_key[at] = key_of<T>(x[i]);
                     sh.list_idx[at] = s0 + i;
                     sh.list_w[at] = R.weight(x[i]);
                 }
@@ -351,88 +479,196 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
             sync();                      // the lists may be written again
             return;
         }
-        // many near-equal logits: their keys' range, then its bits
-        uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-        for (int i = tid; i < n; i += NT)
-            if (here(x[i])) { const uint32_t k = key_of(x[i]); lo = min(lo, k); hi = max(hi, k); }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) { sh.wmin[warp] = lo; sh.wmax[warp] = hi; }
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < NWARP; ++w) { lo = min(lo, sh.wmin[w]); hi = max(hi, sh.wmax[w]); }
-            sh.xch[ex][0] = uint64_t(hi) << 32 | lo;
-        }
-        sync();
-        lo = 0xFFFFFFFFu;
-        hi = 0u;
-        for (int r = 0; r < C; ++r) {
-            const uint64_t v = cl.map_shared_rank(&sh, r)->xch[ex][0];
-            lo = min(lo, uint32_t(v));
-            hi = max(hi, uint32_t(v >> 32));
-        }
-        ex = (ex + 1) & 3;
-        for (int level = 0; level < 5; ++level) {   // 2^32 -> 2^22 -> 2^12 -> 2^2 -> 1 keys
-            int shift = 0;
-            while (shift < 22 && ((hi - lo) >> shift) >= NB) ++shift;
-            histogram(1, [&](float l) { const uint32_t k = key_of(l); return k >= lo && k <= hi ? int((hi - k) >> shift) : -1; });
-            find(1, by_mass, target, cnt, mass);
-            cnt = sh.f_cnt;
-            mass = sh.f_mass;
-            hi -= uint32_t(sh.f_bin) << shift;
-            if (shift == 0) {
-                if (tid == 0) {
-                    const uint64_t w = R.weight(of_key(hi));
-                    const uint32_t all = sh.f_n;
-                    const uint64_t need = by_mass ? (w ? (target - mass + w - 1) / w : all) : target - cnt;
-                    sh.key = hi;
-                    sh.all_eq = all;
-                    sh.n_eq = uint32_t(need < all ? need : all);
-                    sh.mass = mass + sh.n_eq * w;
-                }
-                __syncthreads();
-                return;
-            }
-            lo = max(lo, hi - ((1u << shift) - 1u));
-        }
     };
+
+    const float min_p = A.min_p ? A.min_p[row] : 0.f;
+    const uint64_t wmin = min_p > 0.f ? uint64_t(ceil(double(fminf(min_p, 1.f)) * double(1ull << FRAC))) : 0ull;
+    const float uf = A.u[row];
+    const uint64_t U = uf >= 1.f ? ~0ull : uf > 0.f ? uint64_t(double(uf) * 18446744073709551616.0) : 0ull;
+    // the least mass that is at least p of `mass`, and at least one token's
+    auto p_target = [&](uint64_t mass) {
+        const uint64_t P = top_p > 0.f ? uint64_t(double(top_p) * 18446744073709551616.0) : 0ull;
+        const uint64_t t = __umul64hi(mass, P) + (mass * P != 0ull ? 1ull : 0ull);
+        return t ? t : 1ull;
+    };
+    auto choose = [&](int token, uint64_t w, uint64_t total) {
+        A.tokens[row] = token;
+        if (A.tokens2) A.tokens2[row] = token;
+        if (A.probs) A.probs[row] = float(double(w) / double(total));
+    };
+    // warp `warp` holds elements [i0, i1) of the slice where order matters
+    const int per = (n + NWARP * 32 - 1) / (NWARP * 32) * 32;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+
+    if (use_k && top_k <= KLIM) {
+        // ---- sorted path: the bins that hold the first top_k tokens go to CTA 0
+        for (int i = tid; i < NB; i += NT) sh.h[0][i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < n; i += NT) atomicAdd(&sh.h[0][bin_of(R.y(x[i]))], 1u);
+        sync();
+        uint32_t c[2] = {0u, 0u}, earlier[2] = {0u, 0u};
+        for (int r = 0; r < C; ++r) {
+            const uint2 v = *reinterpret_cast<const uint2*>(&cl.map_shared_rank(&sh, r)->h[0][2 * tid]);
+            c[0] += v.x;
+            c[1] += v.y;
+            if (r < rank) { earlier[0] += v.x; earlier[1] += v.y; }
+        }
+        uint64_t all;
+        uint32_t before = uint32_t(block_prefix(c[0] + c[1], all));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (before < uint32_t(top_k) && uint32_t(top_k) <= before + c[j]) { sh.f_bin = 2 * tid + j; sh.f_n = before + c[j]; }
+            before += c[j];
+        }
+        __syncthreads();
+        const int b = sh.f_bin, nc = int(sh.f_n);
+        if (nc <= CAP) {
+            uint32_t base = uint32_t(block_sum((2 * tid <= b ? earlier[0] : 0u) + (2 * tid + 1 <= b ? earlier[1] : 0u)));
+            // the candidates in index order
+            uint32_t mine = 0;
+            const float yend = b < NB - 1 ? float(b + 1) : INFINITY;   // bin <= b: 16 y below b + 1
+            auto in_bins = [&](float l) { return b == NB - 1 || R.y(l) * 16.f < yend; };
+            for (int i = i0 + lane; i < i1; i += 32) mine += in_bins(x[i]);
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) sh.wcnt[warp] = mine;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) base += sh.wcnt[w];
+            Shared* o = cl.map_shared_rank(&sh, 0);
+            for (int i = i0; i < i1; i += 32) {
+                const float l = i + lane < i1 ? x[i + lane] : 0.f;
+                const bool in = i + lane < i1 && in_bins(l);
+                const uint32_t hit = __ballot_sync(0xffffffffu, in);
+                if (in) {
+                    const uint32_t at = base + __popc(hit & ((1u << lane) - 1u));
+                    o->h[1][at] = key_of<T>(l);
+                    o->h[2][at] = uint32_t(s0 + i + lane);
+                    o->fm[0][at] = R.weight(l);
+                }
+                base += __popc(hit);
+            }
+            sync();
+            if (rank != 0) return;       // CTA 0 reads its own shared memory alone from here on
+            int np = 64;
+            while (np < nc) np *= 2;
+            for (int i = tid; i < np; i += NT) sh.fm[1][i] = i < nc ? uint64_t(~sh.h[1][i]) << 32 | uint32_t(i) : ~0ull;
+            __syncthreads();
+            // bitonic sort, ascending: logit descending, index ascending
+            for (int k = 2; k <= np; k *= 2)
+                for (int j = k / 2; j > 0; j /= 2) {
+                    if (tid < np / 2) {
+                        const int i = ((tid & ~(j - 1)) << 1) | (tid & (j - 1));
+                        const uint64_t lo = sh.fm[1][i], hi = sh.fm[1][i | j];
+                        if ((lo > hi) == ((i & k) == 0)) { sh.fm[1][i] = hi; sh.fm[1][i | j] = lo; }
+                    }
+                    // a warp's 32 pairs of a step j <= 32 are its own 64 elements; the next step's too
+                    // unless it is a longer one
+                    if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
+                    else __syncwarp();
+                }
+            __syncthreads();
+            int pos[2];
+            uint64_t w[2], total;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = 2 * tid + j;
+                pos[j] = i < nc ? int(uint32_t(sh.fm[1][i])) : -1;
+                w[j] = i < nc && i < top_k ? sh.fm[0][pos[j]] : 0ull;   // the first top_k
+            }
+            uint64_t mb = block_prefix(w[0] + w[1], total);
+            const uint64_t target = use_p ? p_target(total) : ~0ull;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool keep = mb < target && w[j] >= wmin;
+                mb += w[j];
+                if (pos[j] >= 0) sh.fm[0][pos[j]] = keep ? w[j] : 0ull;
+            }
+            __syncthreads();
+            // the draw, in index order
+#pragma unroll
+            for (int j = 0; j < 2; ++j) w[j] = 2 * tid + j < nc ? sh.fm[0][2 * tid + j] : 0ull;
+            mb = block_prefix(w[0] + w[1], total);
+            const uint64_t draw = __umul64hi(total, U);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (mb <= draw && draw < mb + w[j]) choose(int(sh.h[2][2 * tid + j]), w[j], total);
+                mb += w[j];
+            }
+            return;
+        }
+        __syncthreads();
+    }
 
     // ---- the kept prefix: every logit above `key`, and the n_eq lowest-indexed equal to it
     uint32_t key = 0u, n_eq = 0xFFFFFFFFu, all_eq = 0u;
-    if (use_k || use_p) {
-        histogram(0, [&](float l) { return bin_of(R.y(l)); });
-        uint64_t mass = 0;
-        if (use_k) {
-            select(false, uint64_t(top_k));
-            __syncthreads();
-            mass = sh.mass;
-            key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
-        } else {
-            // all of it
-            find(0, false, uint64_t(A.vocab), 0u, 0ull);
-            mass = sh.f_mass + sh.f_m;
-        }
+    if (use_k) {
+        histogram(0, [&](float l) { return bin_of(R.y(l)); }, std::false_type());
+        select(false, uint64_t(top_k), 0ull);
+        __syncthreads();
+        const uint64_t mass = sh.mass;
+        key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
         if (use_p) {
-            // ceil(p * mass), at least one token
-            const uint64_t P = top_p > 0.f ? uint64_t(double(top_p) * 18446744073709551616.0) : 0ull;
-            uint64_t target = __umul64hi(mass, P) + (mass * P != 0ull ? 1ull : 0ull);
-            if (target == 0) target = 1;
-            select(true, target);
+            select(true, p_target(mass), 0ull);
             __syncthreads();
             key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
         }
+    } else if (use_p) {
+        // masses of the bins to 2^-14: 2^(f / 16) in units of 2^-14, f the distance to the bin's end
+        for (int i = tid; i < NB; i += NT) sh.h[0][i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < n; i += NT) {
+            const float y = R.y(x[i]) * 16.f;
+            if (y < 46.f * 16.f) {
+                const float down = __fadd_rd(y, 8388608.f);
+                float v;                   // in [1, 2^(1/16)]: its first 14 fraction bits
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(fmaf(down - 8388608.f - y, 1.f / 16.f, 1.f / 16.f)));
+                atomicAdd(&sh.h[0][__float_as_int(down) - 0x4B000000], (__float_as_uint(v) - 0x3F000000u) >> 9);
+            }
+        }
+        sync();
+        float q[2] = {0.f, 0.f};
+        for (int r = 0; r < C; ++r) {
+            const uint2 v = *reinterpret_cast<const uint2*>(&cl.map_shared_rank(&sh, r)->h[0][2 * tid]);
+            q[0] += float(v.x);
+            q[1] += float(v.y);
+        }
+        // in units of 2^-40 (at most 2^18 tokens of 2^40): exact sums of what is good to 2^-13
+        uint64_t qi[2], total;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) qi[j] = uint64_t(q[j] * exp2f(26.f - float(2 * tid + j + 1) / 16.f));
+        uint64_t before = block_prefix(qi[0] + qi[1], total);
+        // the prefix ends where the mass passes p of the total: both are within 2^-12
+        const float want = fmaxf(top_p, 0.f) * float(total), t1 = want * (1.f - 1.f / 2048.f), t2 = want * (1.f + 1.f / 2048.f);
+        if (tid == 0) { sh.f_bin = 0; sh.f_n = NB - 1; }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float lo = float(before), hi = float(before + qi[j]);
+            if (lo < t1 && t1 <= hi) sh.f_bin = 2 * tid + j;
+            if (lo < t2 && t2 <= hi) sh.f_n = uint32_t(2 * tid + j);
+            before += qi[j];
+        }
+        __syncthreads();
+        const int b1 = sh.f_bin, b2 = int(sh.f_n);
+        __syncthreads();
+        histogram(0, [&](float l) { const int b = bin_of(R.y(l)); return b < b1 ? ABOVE : b > b2 ? BELOW : b; }, std::true_type());
+        const uint64_t head = above;
+        uint64_t inside;
+        {
+            const Shared* o = cl.map_shared_rank(&sh, (2 * tid) / (NB / C));
+            inside = block_sum(o->fm[0][2 * tid] + o->fm[0][2 * tid + 1]);
+        }
+        select(true, p_target(above + inside + below), head);
+        __syncthreads();
+        key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
     }
-    const float min_p = A.min_p ? A.min_p[row] : 0.f;
-    const uint64_t wmin = min_p > 0.f ? uint64_t(ceil(double(fminf(min_p, 1.f)) * double(1ull << FRAC))) : 0ull;
 
-    // ---- masses in index order: warp `warp` holds elements [i0, i1) of the slice
-    const int per = (n + NWARP * 32 - 1) / (NWARP * 32) * 32;
-    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+    // ---- masses in index order
     uint32_t eq0 = 0;                    // equal tokens before this warp's
     const bool ties = n_eq < all_eq;
     if (ties) {
         uint32_t c = 0;
-        for (int i = i0 + lane; i < i1; i += 32) c += key_of(x[i]) == key;
+        for (int i = i0 + lane; i < i1; i += 32) c += key_of<T>(x[i]) == key;
         c = __reduce_add_sync(0xffffffffu, c);
         __syncthreads();
         if (lane == 0) sh.wcnt[warp] = c;
@@ -447,11 +683,13 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         for (int w = 0; w < warp; ++w) eq0 += sh.wcnt[w];
         ex = (ex + 1) & 3;
     }
+    // past this y a weight is below min_p (half a percent more, for the rounding of both)
+    const float ymax = min_p > 0.f ? -log2f(fminf(min_p, 1.f)) * 1.005f + 0.005f : INFINITY;
     // kept mass of element i (lanes in index order); eq: equal tokens before this group of 32
     auto kept = [&](int i, uint32_t& eq) -> uint64_t {
         const float l = i < i1 ? x[i] : -INFINITY;
-        const uint32_t k = key_of(l);
-        bool keep = i < i1 && k >= key;
+        const uint32_t k = key_of<T>(l);
+        bool keep = i < i1 && k >= key && R.y(l) < ymax;
         if (ties) {
             const uint32_t same = __ballot_sync(0xffffffffu, i < i1 && k == key);
             if (k == key) keep = keep && eq + __popc(same & ((1u << lane) - 1u)) < n_eq;
@@ -483,8 +721,6 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         total += v;
     }
     for (int w = 0; w < warp; ++w) start += sh.wsum[w];
-    const float uf = A.u[row];
-    const uint64_t U = uf >= 1.f ? ~0ull : uf > 0.f ? uint64_t(double(uf) * 18446744073709551616.0) : 0ull;
     const uint64_t target = __umul64hi(total, U);
     if (start <= target && target < start + sum) {       // this warp holds the crossing
         uint32_t eq = eq0;
@@ -498,11 +734,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
             }
             const uint32_t hit = __ballot_sync(0xffffffffu, start + inc > target);
             if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    A.tokens[row] = s0 + i + lane;
-                    if (A.tokens2) A.tokens2[row] = s0 + i + lane;
-                    if (A.probs) A.probs[row] = float(double(w) / double(total));
-                }
+                if (lane == __ffs(hit) - 1) choose(s0 + i + lane, w, total);
                 break;
             }
             start += __shfl_sync(0xffffffffu, inc, 31);
@@ -542,10 +774,10 @@ cudaError_t launch(const SampleArgs& a, int C, int S, cudaStream_t st) {
 }  // namespace
 
 extern "C" cudaError_t kie_launch_sample(const SampleArgs* a, int sms, cudaStream_t st) {
-    // CTAs per row: enough to fill the GPU with few rows, and at least so many
-    // that a slice fits shared memory
+    // CTAs per row: enough to fill the GPU (two per SM) with few rows, and at least so
+    // many that a slice fits shared memory; a slice below 1,024 gains nothing more
     int C = 1;
-    while (C < MAXC && (int64_t(a->rows) * C < sms || int64_t(a->vocab) > int64_t(C) * 32768) && a->vocab > C * 1024) C *= 2;
+    while (C < MAXC && (int64_t(a->rows) * C < 2 * sms || int64_t(a->vocab) > int64_t(C) * 32768) && a->vocab > C * 1024) C *= 2;
     const int S = ((a->vocab + C - 1) / C + 7) / 8 * 8;
     if (a->type == 0) return launch<0>(*a, C, S, st);
     if (a->type == 1) return launch<1>(*a, C, S, st);
