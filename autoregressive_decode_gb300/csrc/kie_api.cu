@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1772,20 +1773,24 @@ namespace {
 // Makes `device` current and restores the caller's device at the end.
 struct DeviceScope {
     int before = -1;
-    bool ok = false;
+    bool ok = false, changed = false;
     explicit DeviceScope(int device) {
         if (cudaGetDevice(&before) != cudaSuccess) { before = -1; cudaGetLastError(); return; }
-        ok = before == device || cudaSetDevice(device) == cudaSuccess;
+        changed = before != device;
+        ok = !changed || cudaSetDevice(device) == cudaSuccess;
         if (!ok) cudaGetLastError();
     }
     ~DeviceScope() {
-        if (before >= 0) cudaSetDevice(before);
+        if (ok && changed) cudaSetDevice(before);
     }
 };
 
 int sm_count(int device) {
-    int n = 0;
+    static std::atomic<int> known[64];      // 0: not asked yet
+    int n = device >= 0 && device < 64 ? known[device].load(std::memory_order_relaxed) : 0;
+    if (n) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) { cudaGetLastError(); return 0; }
+    if (device >= 0 && device < 64) known[device].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -1847,6 +1852,24 @@ const char* kv4_query_error(const kie_kv4_cache* c, const kie_kv4_query* q) {
     return nullptr;
 }
 
+Kv4Attn kv4_attn(const kie_kv4_cache* c, const kie_kv4_query* q) {
+    Kv4Attn a{};
+    a.c = kv4_of(c);
+    a.q = q->q;
+    a.out = q->out;
+    a.qs = strides_of(q->q_strides, q->n_tokens, q->n_heads, c->head_dim);
+    a.os = strides_of(q->out_strides, q->n_tokens, q->n_heads, c->head_dim);
+    a.type = q->dtype;
+    a.heads = q->n_heads;
+    a.n_q = q->n_tokens;
+    a.kv_len = q->kv_len;
+    a.n_tok = q->n_tok;
+    a.causal = q->causal;
+    a.window = q->window;
+    a.scale = q->scale;
+    return a;
+}
+
 }  // namespace
 
 size_t kie_kv4_bytes(const kie_kv4_cache* c) {
@@ -1890,8 +1913,9 @@ size_t kie_kv4_attention_workspace(const kie_kv4_cache* c, const kie_kv4_query* 
     if (kv4_query_error(c, q)) return 0;
     const int sms = sm_count(c->device);
     if (sms < 1) return 0;
-    const Kv4 kv = kv4_of(c);
-    return kie_kv4_attention_ws_floats(&kv, q->n_heads, q->n_tokens, q->dtype, sms) * 4;
+    const Kv4Attn a = kv4_attn(c, q);
+    // at least the alignment: 0 says that the query is invalid
+    return std::max<size_t>(16, kie_kv4_attention_ws_floats(&a, sms) * 4);
 }
 
 kie_status kie_kv4_attention(const kie_kv4_cache* c, const kie_kv4_query* q, void* workspace, size_t ws_bytes,
@@ -1910,23 +1934,10 @@ kie_status kie_kv4_attention(const kie_kv4_cache* c, const kie_kv4_query* q, voi
     if (!dev.ok) return fail(nullptr, KIE_ERR_CUDA, "cudaSetDevice(%d) failed", c->device);
     const int sms = sm_count(c->device);
     if (sms < 1) return fail(nullptr, KIE_ERR_CUDA, "no multiprocessor count");
-    Kv4Attn a{};
-    a.c = kv4_of(c);
-    const size_t need = kie_kv4_attention_ws_floats(&a.c, q->n_heads, q->n_tokens, q->dtype, sms) * 4;
-    if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+    Kv4Attn a = kv4_attn(c, q);
+    const size_t need = kie_kv4_attention_ws_floats(&a, sms) * 4;
+    if (need && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
         return fail(nullptr, KIE_ERR_OOM, "workspace too small or misaligned (need %zu bytes)", need);
-    a.q = q->q;
-    a.out = q->out;
-    a.qs = strides_of(q->q_strides, q->n_tokens, q->n_heads, c->head_dim);
-    a.os = strides_of(q->out_strides, q->n_tokens, q->n_heads, c->head_dim);
-    a.type = q->dtype;
-    a.heads = q->n_heads;
-    a.n_q = q->n_tokens;
-    a.kv_len = q->kv_len;
-    a.n_tok = q->n_tok;
-    a.causal = q->causal;
-    a.window = q->window;
-    a.scale = q->scale;
     a.ws = static_cast<float*>(workspace);
     KIE_CUDA(nullptr, kie_launch_kv4_attention(&a, sms, static_cast<cudaStream_t>(stream)));
     return KIE_OK;

@@ -60,6 +60,7 @@ extern "C" cudaError_t kie_launch_kv4_append(const Kv4* c, const void* k, const 
 extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const Kv4Strides* ks, const Kv4Strides* vs,
                                            int type, int n, const int32_t* start, const int32_t* n_tok,
                                            cudaStream_t st);
-// Floats of workspace the attention needs on a GPU with `sms` SMs.
-extern "C" size_t kie_kv4_attention_ws_floats(const Kv4* c, int heads, int n_q, int type, int sms);
+// Floats of workspace that the attention needs on a GPU with `sms` SMs (0 for most
+// single-token calls); the pointers of `a` are not looked at.
+extern "C" size_t kie_kv4_attention_ws_floats(const Kv4Attn* a, int sms);
 extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaStream_t st);

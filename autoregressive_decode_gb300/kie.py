@@ -383,13 +383,15 @@ def convert_fp8_e5m2(x16: np.ndarray) -> np.ndarray:
 # device (or on `stream`, a torch.cuda.Stream).  Results are allocated by torch
 # where `out` is not given.
 _torch = None
+_raw_stream = None
 DTYPES = {}      # torch dtype -> kie_dtype
 
 
 def _need_torch():
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # what current_stream() wraps
         DTYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
         _torch = torch
     return _torch
@@ -438,7 +440,9 @@ def _written(t, what):
 
 
 def _stream(stream, device):
-    return (_torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device) if _raw_stream is not None else _torch.cuda.current_stream(device).cuda_stream
 
 
 class KV4Cache:
@@ -459,7 +463,7 @@ class KV4Cache:
         self.desc.data = self.data.data_ptr()
         self.batch, self.n_kv_heads, self.max_ctx, self.head_dim = batch, n_kv_heads, max_ctx, head_dim
         self.group, self.device = group, index
-        self._ws_bytes = {}      # (tokens, heads, dtype) -> kie_kv4_attention_workspace
+        self._ws_bytes = {}      # (tokens, heads, dtype, window) -> kie_kv4_attention_workspace
 
     def append(self, k, v, start, n_tok=None, stream=None):
         """kie_kv4_append: store k, v [batch, tokens, n_kv_heads, head_dim] (any
@@ -522,13 +526,19 @@ class KV4Cache:
         a = kie_kv4_query(qp, op, None if qs is None else C.addressof(qs), None if os_ is None else C.addressof(os_),
                           _vector(kv_len, b, i32, dev, "kv_len"), _vector(n_tok, b, i32, dev, "n_tok"), dt, n, heads,
                           bool(causal), window, self.head_dim ** -0.5 if scale is None else scale)
-        need = self._ws_bytes.get((n, heads, dt))
+        key = (n, heads, dt, window)
+        need = self._ws_bytes.get(key)
         if need is None:
-            need = self._ws_bytes[n, heads, dt] = _lib.kie_kv4_attention_workspace(self.desc, a)
-        # of this call: the allocator gives it to no one else before the stream is
-        # done with it, and a captured graph keeps its own
-        ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
-        _check(_lib.kie_kv4_attention(self.desc, a, ws.data_ptr(), need, _stream(None, dev)))
+            if len(self._ws_bytes) > 1000:
+                self._ws_bytes.clear()
+            need = self._ws_bytes[key] = _lib.kie_kv4_attention_workspace(self.desc, a)
+        if need > 16:
+            # of this call: the allocator gives it to no one else before the stream
+            # is done with it, and a captured graph keeps its own
+            ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
+            _check(_lib.kie_kv4_attention(self.desc, a, ws.data_ptr(), need, _stream(None, dev)))
+        else:
+            _check(_lib.kie_kv4_attention(self.desc, a, None, 0, _stream(None, dev)))
         return out
 
 

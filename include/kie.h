@@ -440,12 +440,13 @@ typedef struct {
     float scale;
 } kie_kv4_query;
 
-/* Device bytes that kie_kv4_attention needs for a query of this shape (dtype,
- * n_tokens and n_heads are looked at); 0 for an invalid one. */
+/* Device bytes that kie_kv4_attention needs for this query (its pointers are not
+ * looked at): at most 16 where it needs none, 0 for an invalid query. */
 size_t kie_kv4_attention_workspace(const kie_kv4_cache* c, const kie_kv4_query* q);
 
 /* workspace: device memory of at least kie_kv4_attention_workspace() bytes,
- * 16-byte aligned, for this call alone until its work on `stream` is done. */
+ * 16-byte aligned, for this call alone until its work on `stream` is done (may be
+ * NULL where that is at most 16). */
 kie_status kie_kv4_attention(const kie_kv4_cache* c, const kie_kv4_query* q, void* workspace, size_t ws_bytes,
                              void* stream);
 
