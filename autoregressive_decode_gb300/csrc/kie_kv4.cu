@@ -1120,6 +1120,11 @@ Plan plan_of(const Kv4Attn& a, int sms) {
     return p;
 }
 
+// Whether the kernel of 128-row tiles takes the call.
+bool many_tokens(const Kv4Attn& a) {
+    return a.type == KV4_BF16 && int64_t(a.n_q) * (a.heads / a.c.heads) >= 64;
+}
+
 template <int D, int NG, int MODE, int T>
 cudaError_t launch_attention(AttnArgs A, const Plan& p, cudaStream_t st) {
     constexpr int RT = rows_of(MODE);
@@ -1212,11 +1217,13 @@ extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const
 // i: a CTA's items and an item's CTAs are both consecutive, so no two (item, CTA)
 // pairs that meet share a slot.  The cluster form needs none.
 extern "C" size_t kie_kv4_attention_ws_floats(const Kv4Attn* a, int sms) {
+    if (many_tokens(*a)) return kie_kv4_chunk_ws_floats(a, sms);
     const Plan p = plan_of(*a, sms);
     return p.S ? 0 : size_t(p.items + p.nctas) * rows_of(p.mode) * (a->c.dim + 2);
 }
 
 extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaStream_t st) {
+    if (many_tokens(*a)) return kie_launch_kv4_chunk(a, sms, st);
     const Plan p = plan_of(*a, sms);
     const AttnArgs A{*a, p.per, p.nrt, p.nctas};
     const int ng = a->c.dim / a->c.group;
