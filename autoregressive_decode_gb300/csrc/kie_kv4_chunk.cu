@@ -1,22 +1,26 @@
 // Attention of many new tokens (prompt chunks, long drafts) over the 4-bit K/V
 // cache, on the 5th-generation tensor cores; see kie_kv4.cu for few tokens.
 //
-// One CTA takes 128 query rows (tokens x the query heads that share a K/V head) of
-// one request and one stretch of the keys, two CTAs per SM, so that one's tensor
-// work fills the other's softmax.  Per tile of 128 keys:
-//   warps 4-7   thread = key: codes from global memory (a tile ahead, in registers)
-//               to fp16 values code * s + z, rounded once, into the K and V tiles;
-//   warp 4      also issues S = Q K^T and O += P V (tcgen05.mma, M 128), S and O in TMEM;
-//   warps 0-3   thread = query row: running maximum, P = 2^(S - m) as fp16 over the
-//               first half of S's columns, running sum; O is rescaled only when a
-//               maximum grew by more than 2^8 (exact either way: m is any
-//               reference, fp16 holds 2^15).
+// One CTA takes two tiles of 128 query rows (tokens x the query heads that share a
+// K/V head) of one request and one stretch of the keys.  Per tile of 128 keys:
+//   warps 16-19  thread = key: codes from global memory (a tile ahead, in registers)
+//                to fp16 values code * s + z, rounded once, into K and V tiles, two
+//                of each in flight, shared by both row tiles;
+//   warps 0, 8   one thread each issues its row tile's S = Q K^T and O += P V
+//                (tcgen05.mma, M 128), S and O in TMEM;
+//   warps 0-15   two threads per query row, 64 keys each: running maximum, P =
+//                2^(S - m) as fp16 over the first half of its S columns, running sum;
+//                O is rescaled only when a maximum grew by more than 2^8 (exact
+//                either way: m is any reference, and fp16 holds 2^15).
+// The row tiles take turns: while one's softmax runs, the tensor pipe has the other's
+// two products (PV of one key tile, S of the next).  P overlies S, so that the next S
+// waits for the product that reads P: the order of two tcgen05.mma with different
+// accumulators is not guaranteed otherwise.
 // Tiles use the canonical no-swizzle layouts, K as rows of channels (K-major), V as
-// stored (MN-major).  Within 8 channels the order is 0 4 1 5 2 6 3 7, in which the
-// nibbles of a word come apart; Q is stored alike and O's columns are read alike.
+// stored (MN-major); the pipe runs them at its full rate (64 cycles an instruction).
+// Within 8 channels the order is 0 4 1 5 2 6 3 7, in which the nibbles of a word come
+// apart; Q is stored alike and O's columns are read alike.
 //
-// The tensor pipe needs 1,024 cycles per tile and CTA; unpacking (2,100 warp
-// instructions) and softmax (1,600) need about as many issue slots.
 // Rounding: K, V and P to fp16 (2^-12 relative on average less), 16 times finer
 // than the bf16 results this serves.
 #include <cuda_bf16.h>
@@ -33,8 +37,8 @@ using namespace kie;
 namespace {
 
 constexpr int KEYS = 128;             // keys per tile
-constexpr int ROWS = 128;             // query rows per CTA
-constexpr int THREADS = 256;
+constexpr int ROWS = 256;             // query rows per CTA, in two tiles
+constexpr int THREADS = 640;
 constexpr int WAIT_TRIES = 100000;    // of up to 20 us each: 2 s, then the rows become NaN
 constexpr float LAZY = 8.f;           // log2 of the growth of a maximum that is left alone
 constexpr float UP = 7.f;             // p is at most 2^(LAZY + UP): fp16's range
@@ -48,12 +52,15 @@ template <int D>
 struct Sm {
     static constexpr uint32_t SBO = (D / 8) * 128;                       // 8 rows of a K-major tile (8 keys of V)
     static constexpr uint32_t TILE = 128 * D * 2;
-    static constexpr uint32_t Q = 0, K = TILE, V = 2 * TILE, BARS = 3 * TILE;
-    static constexpr uint32_t RAW = BARS + 128;
-    // never three CTAs on an SM: TMEM holds two
-    static constexpr uint32_t BYTES = RAW > 80 * 1024 ? RAW : 80 * 1024;
+    static constexpr uint32_t Q = 0, K = 2 * TILE, V = 4 * TILE, BARS = 6 * TILE;
+    static constexpr uint32_t MAXES = BARS + 256;                        // [parity][row tile][half][128]
+    static constexpr uint32_t SUMS = MAXES + 2 * 2 * 2 * 128 * 4;        // [row tile][half][128]
+    static constexpr uint32_t USED = SUMS + 2 * 2 * 128 * 4;
+    // never two CTAs on an SM: one takes all of TMEM
+    static constexpr uint32_t BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
 };
-enum { KFULL = 0, KFREE, VFULL, VFREE, SFULL, PFULL, NBARS };
+// [2]: per stage (K, V) or row tile (S, P, PV)
+enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, PVDONE = 12, FIN = 14, NBARS = 15 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* failed) {
     for (int i = 0; i < WAIT_TRIES; ++i) {
@@ -64,12 +71,36 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
     return false;
 }
 
-// A operand (P, fp16 pairs in 32-bit columns) from TMEM, B from shared memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The tensor instructions are issued by whole warps under a predicate that one lane
+// holds: their descriptors then stay in uniform registers (a branch to one thread
+// costs a transfer per operand, 150 cycles an instruction beside four busy warps).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p;
+}
+// D[tmem] (+)= A B^T, A and B from shared memory.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t el) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(el), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+// A (P, fp16 pairs in 32-bit columns) from TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t el) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t el) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"(el)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
@@ -79,6 +110,24 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+// 16 columns of this warp's TMEM lanes without waiting; and the wait for every load,
+// through which the registers go, so that no use of them moves before it.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+        :: "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -87,6 +136,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -132,15 +186,17 @@ struct Raw {
 };
 
 template <int D, int NG, int T>
-__global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A) {
+__global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A) {
     using E = typename El<T>::type;
     using L = Sm<D>;
-    constexpr int BLK = D / 32, BPG = BLK / NG, NC = D / 32;      // 16-byte loads of a key's codes
+    constexpr int BLK = D / 32, BPG = BLK / NG, NC = D / 32;      // NC: 16-byte loads of a key's codes
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BARS);
     uint32_t* taddr = reinterpret_cast<uint32_t*>(bar + NBARS);
     volatile int* failed = reinterpret_cast<volatile int*>(taddr + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float* maxes = reinterpret_cast<float*>(sm + L::MAXES);
+    float* sums = reinterpret_cast<float*>(sm + L::SUMS);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // uniform to the compiler
     const Kv4& c = A.a.c;
 
     // later row tiles see more keys: they go first
@@ -151,6 +207,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
     const int n_new = A.a.n_tok ? min(max(__ldg(A.a.n_tok + b), 0), A.a.n_q) : A.a.n_q;
     const int rows = n_new * A.per;
     if (r0 >= rows) return;
+    const int ntl = r0 + 128 < rows ? 2 : 1;       // row tiles with rows
     int lo = 0, hi = len;
     if (A.a.causal) {
         const int t0 = r0 / A.per, t1 = (min(r0 + ROWS, rows) - 1) / A.per;
@@ -163,23 +220,29 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
     const int base = (lo / KEYS + first) * KEYS;
 
     if (tid == 0) {
-        mbar_init(&bar[KFULL], 4);
-        mbar_init(&bar[KFREE], 1);
-        mbar_init(&bar[VFULL], 4);
-        mbar_init(&bar[VFREE], 1);
-        mbar_init(&bar[SFULL], 1);
-        mbar_init(&bar[PFULL], 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[KFULL + i], 4);
+            mbar_init(&bar[KFREE + i], ntl);
+            mbar_init(&bar[VFULL + i], 4);
+            mbar_init(&bar[VFREE + i], ntl);
+            mbar_init(&bar[SFULL + i], 1);
+            mbar_init(&bar[PFULL + i], 8);
+            mbar_init(&bar[PVDONE + i], 1);
+        }
+        mbar_init(&bar[FIN], ntl);
         *failed = 0;
         mbar_fence_init();
     }
-    if (warp == 4) tmem_alloc(taddr, 256);
+    if (warp == 16) tmem_alloc(taddr, 512);
 
-    // ---- Q: thread = row; a power of two brings the row's largest element to [1, 2)
-    const int r = r0 + tid;                        // warps 0-3
-    const bool have = tid < ROWS && r < rows;
+    // ---- Q: a power of two brings a row's largest element to [1, 2)
+    // softmax thread: row tile t, half h of the keys, row `lr` of the tile
+    const int t = warp >> 3, h = (warp >> 2) & 1, lr = (warp & 3) * 32 + lane;
+    const int r = r0 + t * 128 + lr;
+    const bool have = warp < 16 && r < rows;
     const int tok = have ? r / A.per : 0, hq = head * A.per + (have ? r - tok * A.per : 0);
     float cq = 0.f;                                // from S to log2 units
-    if (warp < 4) {
+    if (warp < 16) {
         const E* q = static_cast<const E*>(A.a.q) + b * A.a.qs.b + tok * A.a.qs.t + hq * A.a.qs.h;
         const bool vec = (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
         auto load = [&](int i) {
@@ -205,14 +268,15 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
         const int ex = min(max(((__float_as_int(mx) >> 23) & 255) - 127, -100), 114);
         const float up = copysignf(__int_as_float((127 - ex) << 23), A.a.scale);
         cq = fmaxf(fabsf(A.a.scale) * 1.4426950408889634f * __int_as_float((127 + ex) << 23), 1.2e-38f);
+        uint8_t* dst = sm + L::Q + t * L::TILE + (lr >> 3) * L::SBO + (lr & 7) * 16;
 #pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-            const uint4 raw = load(i);         // from L1
+        for (int i = h * (D / 16); i < (h + 1) * (D / 16); ++i) {        // this half's channels, from L1
+            const uint4 raw = load(i);
             const E* e = reinterpret_cast<const E*>(&raw);
             float f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = El<T>::to(e[j]) * up;
-            *reinterpret_cast<uint4*>(sm + L::Q + (tid >> 3) * L::SBO + i * 128 + (tid & 7) * 16) =
+            *reinterpret_cast<uint4*>(dst + i * 128) =
                 make_uint4(pack_h2(f[0], f[4]), pack_h2(f[1], f[5]), pack_h2(f[2], f[6]), pack_h2(f[3], f[7]));
         }
         fence_proxy_async_shared();
@@ -220,38 +284,37 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tS = *taddr, tO = tS + 128u;
+    const uint32_t tmem = *taddr;                  // S of the row tiles at 0 and 128, O at 256 and 384
 
-    if (warp >= 4) {
+    float m = -INFINITY, l = 0.f;
+    if (warp >= 16) {
         // ---- codes to tiles: thread = key
-        const int k = tid - 128;
+        const int k = tid - 512;
         const size_t row0 = (size_t(b) * c.heads + head) * c.ctx_pad;
-        auto load = [&](int i, Raw<D, NG>& K, Raw<D, NG>& V) {
+        Raw<D, NG> K, V;
+        auto load_k = [&](int i) {
             const int p = min(base + i * KEYS + k, c.ctx_pad - 1);   // in the head's memory; zeroed below where not stored
             const uint4* kc = reinterpret_cast<const uint4*>(c.kc + (row0 + p) * (D / 2));
-            const uint4* vc = reinterpret_cast<const uint4*>(c.vc + (row0 + p) * (D / 2));
-#pragma unroll
-            for (int j = 0; j < NC; ++j) { K.c[j] = __ldg(kc + j); V.c[j] = __ldg(vc + j); }
             const uint32_t* kp = reinterpret_cast<const uint32_t*>(c.kp) + (row0 + p) * NG;
-            const int rr = p & 7, t = rr >> 2 ? 7 - rr : rr;
-            const uint32_t* vp = reinterpret_cast<const uint32_t*>(c.vp) + ((row0 + p) >> 3) * (8 * NG) + t * 2 * NG;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) K.c[j] = __ldg(kc + j);
 #pragma unroll
             for (int j = 0; j < NG; ++j) K.p[j] = __ldg(kp + j);
+        };
+        auto load_v = [&](int i) {
+            const int p = min(base + i * KEYS + k, c.ctx_pad - 1);
+            const uint4* vc = reinterpret_cast<const uint4*>(c.vc + (row0 + p) * (D / 2));
+            const int rr = p & 7, pt = rr >> 2 ? 7 - rr : rr;
+            const uint32_t* vp = reinterpret_cast<const uint32_t*>(c.vp) + ((row0 + p) >> 3) * (8 * NG) + pt * 2 * NG;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) V.c[j] = __ldg(vc + j);
 #pragma unroll
             for (int j = 0; j < 2 * NG; ++j) V.p[j] = __ldg(vp + j);
         };
-        Raw<D, NG> K, V;
-        constexpr uint32_t IS = (1u << 4) | (uint32_t(KEYS >> 3) << 17) | (uint32_t(ROWS >> 4) << 24);
-        constexpr uint32_t IO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(ROWS >> 4) << 24);
-        const bool issuer = tid == 128;
-        int issued_s = 0, issued = 0;
-        if (ntile > 0) load(0, K, V);
-        for (int i = 0; i < ntile; ++i) {
-            const int p = base + i * KEYS + k;
-            const bool stored = p < len;
-            const uint32_t ph = uint32_t(i) & 1u;
-            if (__any_sync(0xffffffffu, i > 0 && !wait_for(&bar[KFREE], ph ^ 1u, failed))) break;
-            uint8_t* dst = sm + L::K + (k >> 3) * L::SBO + (k & 7) * 16;
+        const uint32_t at = (k >> 3) * L::SBO + (k & 7) * 16;
+        auto put_k = [&](int i) {
+            const bool stored = base + i * KEYS + k < len;
+            uint8_t* dst = sm + L::K + (i & 1) * L::TILE + at;
 #pragma unroll
             for (int bl = 0; bl < BLK; ++bl) {
                 // scale and zero of the block's group, doubled
@@ -259,155 +322,213 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
                 const uint32_t sw = NG == 1 ? K.p[0] : K.p[gi >> 1], zw = NG == 1 ? K.p[0] : K.p[NG / 2 + (gi >> 1)];
                 const uint32_t s2 = stored ? __byte_perm(sw, 0u, (NG > 1 && (gi & 1)) ? 0x3232 : 0x1010) : 0u;
                 const uint32_t z2 = stored ? __byte_perm(zw, 0u, (NG == 1 || (gi & 1)) ? 0x3232 : 0x1010) : 0u;
-                // word t * BLK + bl of the key: channels 32 bl + 8 t ..
+                // word j * BLK + bl of the key: channels 32 bl + 8 j ..
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int wi = t * BLK + bl;
+                for (int j = 0; j < 4; ++j) {
+                    const int wi = j * BLK + bl;
                     const uint4& q = K.c[wi >> 2];
                     const uint32_t w = (wi & 3) == 0 ? q.x : (wi & 3) == 1 ? q.y : (wi & 3) == 2 ? q.z : q.w;
-                    *reinterpret_cast<uint4*>(dst + (bl * 4 + t) * 128) = values8(w, s2, z2);
+                    *reinterpret_cast<uint4*>(dst + (bl * 4 + j) * 128) = values8(w, s2, z2);
                 }
             }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[KFULL]);
-            // S overlies P and V is read by the same product: the last one has to be done
-            bool ok = i == 0 || wait_for(&bar[VFREE], ph ^ 1u, failed);
-            if (issuer && ok && (ok = wait_for(&bar[KFULL], ph, failed))) {
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_f16(tS, smem_desc_noswz(sm + L::Q + kk * 256, 128, L::SBO), smem_desc_noswz(sm + L::K + kk * 256, 128, L::SBO),
-                               IS, kk != 0 ? 1u : 0u);
-                tc_commit(&bar[SFULL]);
-                tc_commit(&bar[KFREE]);
-                issued_s = i + 1;
-            }
-            if (__any_sync(0xffffffffu, !ok)) break;
-            dst = sm + L::V + (k >> 3) * L::SBO + (k & 7) * 16;
-            const uint32_t half = (p & 4) ? 0x3232u : 0x1010u;         // this position of its pair
+        };
+        auto put_v = [&](int i) {
+            const int p = base + i * KEYS + k;
+            const bool stored = p < len;
+            const uint32_t half = (p & 4) ? 0x3232u : 0x1010u;       // this position of its pair, doubled
+            uint8_t* dst = sm + L::V + (i & 1) * L::TILE + at;
 #pragma unroll
             for (int bl = 0; bl < BLK; ++bl) {
                 const int gi = bl / BPG;
                 const uint32_t s2 = stored ? __byte_perm(V.p[gi], 0u, half) : 0u;
                 const uint32_t z2 = stored ? __byte_perm(V.p[NG + gi], 0u, half) : 0u;
-                // units 2 i2 and 2 i2 + 1 of the block: channels 32 bl + 8 i2 ..
+                // units 2 j and 2 j + 1 of the block: channels 32 bl + 8 j ..
 #pragma unroll
-                for (int i2 = 0; i2 < 4; ++i2) {
-                    const int u0 = 2 * i2 * BLK + bl, u1 = u0 + BLK;     // 16-bit units
+                for (int j = 0; j < 4; ++j) {
+                    const int u0 = 2 * j * BLK + bl, u1 = u0 + BLK;     // 16-bit units
                     auto word = [&](int u) {
                         const int wi = u >> 1;
                         const uint4& q = V.c[wi >> 2];
                         return (wi & 3) == 0 ? q.x : (wi & 3) == 1 ? q.y : (wi & 3) == 2 ? q.z : q.w;
                     };
                     const uint32_t w = __byte_perm(word(u0), word(u1), (u0 & 1) ? 0x7632 : 0x5410);
-                    *reinterpret_cast<uint4*>(dst + (bl * 4 + i2) * 128) = values8(w, s2, z2);
+                    *reinterpret_cast<uint4*>(dst + (bl * 4 + j) * 128) = values8(w, s2, z2);
                 }
             }
-            if (i + 1 < ntile) load(i + 1, K, V);
+        };
+        // the tile that used the same stage last is done with it: its parity
+        auto free_ph = [](int i) { return uint32_t((i >> 1) - 1) & 1u; };
+        auto arrive = [&](int bi) {
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[VFULL]);
-            if (issuer && (ok = wait_for(&bar[VFULL], ph, failed) && wait_for(&bar[PFULL], ph, failed))) {
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < KEYS / 16; ++kk)
-                    mma_ts(tO, tS + kk * 8, smem_desc_noswz(sm + L::V + kk * 2 * L::SBO, L::SBO, 128), IO, (i > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(&bar[VFREE]);
-                issued = i + 1;
-            }
-            if (__any_sync(0xffffffffu, !ok)) break;
+            if (lane == 0) mbar_arrive(&bar[bi]);
+        };
+        if (ntile > 0) {
+            load_k(0);
+            load_v(0);
+            put_k(0);
+            arrive(KFULL);
+            if (ntile > 1) load_k(1);
         }
-        // every product has landed before the accumulators are read or given back
-        if (issuer && issued_s > issued) wait_for(&bar[KFREE], uint32_t(issued_s - 1) & 1u, failed);
-        if (issuer && issued) wait_for(&bar[VFREE], uint32_t(issued - 1) & 1u, failed);
-        __syncwarp();
-    }
-    float m = -INFINITY, l = 0.f;
-    const uint32_t my = uint32_t(warp * 32) << 16;       // this warp's TMEM lanes
-    if (warp < 4) {
-        // ---- softmax: thread = row
+        for (int i = 0; i < ntile; ++i) {      // K runs a tile ahead of V
+            if (i + 1 < ntile) {
+                if (__any_sync(0xffffffffu, i > 0 && !wait_for(&bar[KFREE + ((i + 1) & 1)], free_ph(i + 1), failed))) break;
+                put_k(i + 1);
+                arrive(KFULL + ((i + 1) & 1));
+                if (i + 2 < ntile) load_k(i + 2);
+            }
+            if (__any_sync(0xffffffffu, i > 1 && !wait_for(&bar[VFREE + (i & 1)], free_ph(i), failed))) break;
+            put_v(i);
+            arrive(VFULL + (i & 1));
+            if (i + 1 < ntile) load_v(i + 1);
+        }
+    } else if (t < ntl) {
+        // ---- softmax: threads (t, 0, lr) and (t, 1, lr) share a row
+        const uint32_t my = tmem + (uint32_t((warp & 3) * 32) << 16);       // this warp's TMEM lanes
+        const uint32_t ts = my + t * 128, to = my + 256 + t * 128;
         const int last = !have ? -1 : A.a.causal ? len - n_new + tok : len - 1;
         const int firstk = A.a.window > 0 ? last - A.a.window + 1 : 0;
         const int all_lo = __reduce_max_sync(0xffffffffu, have ? firstk : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, have ? last : 1 << 30);
-        for (int i = 0; i < ntile; ++i) {
-            if (__any_sync(0xffffffffu, !wait_for(&bar[SFULL], uint32_t(i) & 1u, failed))) break;
+        // the row tile's products: its first warp issues
+        const bool issuer = (warp & 7) == 0;
+        const uint32_t el = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        constexpr uint32_t IS = (1u << 4) | (uint32_t(KEYS >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+        constexpr uint32_t IO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+        // addresses in units of 16 bytes
+        const uint64_t dq = smem_desc_noswz(sm + L::Q, 128, L::SBO) + t * (L::TILE / 16);
+        const uint64_t dk = smem_desc_noswz(sm + L::K, 128, L::SBO), dv = smem_desc_noswz(sm + L::V, L::SBO, 128);
+        auto ready = [&](int bi, uint32_t ph) { return !__any_sync(0xffffffffu, !wait_for(&bar[bi], ph, failed)); };
+        auto issue_s = [&](int i) {
+            if (!ready(KFULL + (i & 1), uint32_t(i >> 1) & 1u)) return false;
             tc_fence_after();
-            const int p0 = base + i * KEYS;
-            const bool edge = p0 < all_lo || p0 + KEYS - 1 > all_hi;      // uniform over the warp
+            const uint64_t k = dk + (i & 1) * (L::TILE / 16);
+            mma_ss<false>(tm + t * 128, dq, k, IS, el);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk) mma_ss<true>(tm + t * 128, dq + kk * 16, k + kk * 16, IS, el);
+            commit(&bar[SFULL + t], el);
+            commit(&bar[KFREE + (i & 1)], el);
+            return true;
+        };
+        // the second row tile starts when the first has its P, so that they take turns
+        if (issuer && ntile > 0 && (t == 0 || ready(PFULL, 0u))) issue_s(0);
+        for (int i = 0; i < ntile; ++i) {
+            const uint32_t ph = uint32_t(i) & 1u;
+            if (__any_sync(0xffffffffu, !wait_for(&bar[SFULL + t], ph, failed))) break;
+            tc_fence_after();
+            const int p0 = base + i * KEYS + h * 64;
+            const bool edge = p0 < all_lo || p0 + 63 > all_hi;          // uniform over the warp
+            const uint32_t th = ts + h * 64;       // this half's columns: S, then P over the first 32
             float mt = -INFINITY;
+            if (edge) {                            // mask S in place
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t s[16];
+                    tmem_ld_x16(th + q * 16, s);
+                    tmem_wait_ld(s);
+                    const int f = firstk - p0 - q * 16, e1 = last - p0 - q * 16;  // columns f .. e1 are seen
 #pragma unroll
-            for (int c0 = 0; c0 < KEYS; c0 += 32) {
-                uint32_t s[32];
-                tmem_ld_32x32b_x32(tS + my + c0, s);
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (p0 + c0 + e < firstk || p0 + c0 + e > last) s[e] = 0xFF800000u;
+                    for (int e = 0; e < 16; ++e)
+                        if (e < f || e > e1) s[e] = 0xFF800000u;
+                    tmem_st_x16(th + q * 16, s);
                 }
-                float a = __uint_as_float(s[0]), b2 = __uint_as_float(s[1]);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            }
+            uint32_t s[2][16];                     // the next 16 columns land while these are worked on
+            tmem_ld_x16(th, s[0]);
 #pragma unroll
-                for (int e = 2; e < 32; e += 2) { a = max_nan(a, __uint_as_float(s[e])); b2 = max_nan(b2, __uint_as_float(s[e + 1])); }
-                mt = max_nan(mt, max_nan(a, b2));
+            for (int q = 0; q < 4; ++q) {
+                tmem_wait_ld(s[q & 1]);
+                if (q < 3) tmem_ld_x16(th + (q + 1) * 16, s[(q + 1) & 1]);
+                float a[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        a[j] = max3_nan(a[j], __uint_as_float(s[q & 1][e + 2 * j]), __uint_as_float(s[q & 1][e + 2 * j + 1]));
+                mt = max3_nan(mt, a[0], a[1]);
             }
             mt *= cq;
+            float* mx = maxes + ((ph * 2 + t) * 2) * 128 + lr;
+            mx[h * 128] = mt;
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");
+            mt = max_nan(mt, mx[(h ^ 1) * 128]);
             float f = 1.f;
             if (!(mt <= m + LAZY)) {            // also at the first keys and for a NaN
                 f = m == -INFINITY ? 0.f : ex2(m - mt);
                 l *= f;
                 m = mt;
             }
-            if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) {
+            if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {       // the last product is done: this S was issued after it
+#pragma unroll 1
+                for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
                     uint32_t o[32];
-                    tmem_ld_32x32b_x32(tO + my + c0, o);
+                    tmem_ld_32x32b_x32(to + c0, o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st_32x32b_x32(tO + my + c0, o);
+                    tmem_st_32x32b_x32(to + c0, o);
                 }
             }
             const float ref = (m == -INFINITY ? 0.f : m) - UP;
-            float2 sum = make_float2(0.f, 0.f);
+            float2 sum = make_float2(0.f, 0.f), sum2 = sum;
+            tmem_ld_x16(th, s[0]);                 // again, for P
 #pragma unroll
-            for (int c0 = 0; c0 < KEYS; c0 += 32) {
-                uint32_t s[32], h[16];
-                tmem_ld_32x32b_x32(tS + my + c0, s);
-                if (edge) {
+            for (int q = 0; q < 4; ++q) {
+                tmem_wait_ld(s[q & 1]);
+                if (q < 3) tmem_ld_x16(th + (q + 1) * 16, s[(q + 1) & 1]);
+                uint32_t hp[8];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (p0 + c0 + e < firstk || p0 + c0 + e > last) s[e] = 0xFF800000u;
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                for (int e = 0; e < 8; ++e) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1])),
                                                 make_float2(cq, cq), make_float2(-ref, -ref));
                     const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                    sum = __fadd2_rn(sum, p);
-                    h[e] = pack_h2(p.x, p.y);
+                    if (e & 1) sum = __fadd2_rn(sum, p);
+                    else sum2 = __fadd2_rn(sum2, p);
+                    hp[e] = pack_h2(p.x, p.y);
                 }
-                tmem_st_x16(tS + my + c0 / 2, h);     // columns of S that are read already
+                tmem_st_x8(th + q * 8, hp);        // over columns that are read already
             }
-            l += sum.x + sum.y;
+            l += (sum.x + sum.y) + (sum2.x + sum2.y);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[PFULL]);
+            if (lane == 0) mbar_arrive(&bar[PFULL + t]);
+            if (issuer) {
+                if (!ready(VFULL + (i & 1), uint32_t(i >> 1) & 1u) || !ready(PFULL + t, ph)) break;
+                tc_fence_after();
+                const uint64_t v = dv + (i & 1) * (L::TILE / 16);
+                mma_ts(tm + 256 + t * 128, tm + t * 128, v, IO, i > 0 ? 1u : 0u, el);
+#pragma unroll
+                for (int kk = 1; kk < KEYS / 16; ++kk)
+                    mma_ts(tm + 256 + t * 128, tm + t * 128 + (kk >> 2) * 64 + (kk & 3) * 8, v + kk * (2 * L::SBO / 16), IO, 1u, el);
+                commit(&bar[PVDONE + t], el);
+                commit(&bar[VFREE + (i & 1)], el);
+                if (i + 1 < ntile && !(ready(PVDONE + t, ph) && issue_s(i + 1))) break;
+            }
         }
+        // everything issued has landed before the accumulators are read or given back
+        if (issuer) {
+            commit(&bar[FIN], el);
+            wait_for(&bar[FIN], 0u, failed);
+        }
+        __syncwarp();
+        sums[(t * 2 + h) * 128 + lr] = l;
     }
-    __syncthreads();                   // warp 4 has waited for the last product
+    __syncthreads();
     tc_fence_after();
-    if (warp < 4) {
+    if (warp < 16 && t < ntl) {
         const bool bad = *failed != 0;
+        l = sums[(t * 2) * 128 + lr] + sums[(t * 2 + 1) * 128 + lr];
         float* part = A.nsplit > 1 ? A.a.ws + (size_t(item) * A.nsplit + split) * (ROWS * (D + 2)) : nullptr;
         E* op = static_cast<E*>(A.a.out) + b * A.a.os.b + tok * A.a.os.t + hq * A.a.os.h;
         const bool vec = (reinterpret_cast<uintptr_t>(op) & 15u) == 0;
         const float il = bad ? __int_as_float(0x7FC00000) : l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        const uint32_t to = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + t * 128;
+#pragma unroll 1
+        for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
             uint32_t o[32];
-            if (ntile > 0) tmem_ld_32x32b_x32(tO + my + c0, o);
+            if (ntile > 0) tmem_ld_32x32b_x32(to + c0, o);
             else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -422,9 +543,9 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(o[e + at[j]]);
                 if (A.nsplit > 1) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 4)
-                        *reinterpret_cast<float4*>(part + size_t(tid) * D + c0 + e + j) =
-                            bad ? make_float4(il, il, il, il) : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    for (int j = 0; j < 8; j += 2)
+                        *reinterpret_cast<float2*>(part + size_t(t * 128 + lr) * D + c0 + e + j) =
+                            bad ? make_float2(il, il) : make_float2(v[j], v[j + 1]);
                 } else {
                     uint4 w;
                     E* we = reinterpret_cast<E*>(&w);
@@ -438,11 +559,11 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_chunk_kernel(const ChunkArgs A
                 }
             }
         }
-        if (A.nsplit > 1 && have) *reinterpret_cast<float2*>(part + ROWS * D + 2 * tid) = make_float2(m, l);
+        if (A.nsplit > 1 && have && h == 0) *reinterpret_cast<float2*>(part + ROWS * D + 2 * (t * 128 + lr)) = make_float2(m, l);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) tmem_dealloc(tS, 256);
+    if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 // Join the stretches of the keys.  One block per item and 2 rows (D = 128) or 4.
@@ -500,8 +621,8 @@ ChunkPlan plan_of(const Kv4Attn& a, int sms) {
     int64_t keys = a.c.max_ctx;
     if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + ROWS / p.per + 1);
     const int64_t tiles = (keys + KEYS - 1) / KEYS + (a.window > 0);
-    // stretches of at least four tiles until two CTAs per SM are busy
-    p.nsplit = int(std::max<int64_t>(1, std::min<int64_t>(2 * sms / std::max<int64_t>(p.items, 1), tiles / 4)));
+    // stretches of at least four tiles while SMs are left over
+    p.nsplit = int(std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(p.items, 1), tiles / 4)));
     return p;
 }
 
