@@ -2,20 +2,19 @@
 // cache, on the 5th-generation tensor cores; see kie_kv4.cu for few tokens.
 //
 // One CTA takes two tiles of 128 query rows (tokens x the query heads that share a
-// K/V head) of one request and one stretch of the keys.  Per tile of 128 keys:
+// K/V head) of one request and one stretch of the keys, in tiles of 128 keys:
 //   warps 16-19  thread = key: codes from global memory (a tile ahead, in registers)
 //                to fp16 values code * s + z, rounded once, into K and V tiles, two
 //                of each in flight, shared by both row tiles;
-//   warps 0, 8   one thread each issues its row tile's S = Q K^T and O += P V
-//                (tcgen05.mma, M 128), S and O in TMEM;
-//   warps 0-15   two threads per query row, 64 keys each: running maximum, P =
-//                2^(S - m) as fp16 over the first half of its S columns, running sum;
-//                O is rescaled only when a maximum grew by more than 2^8 (exact
-//                either way: m is any reference, and fp16 holds 2^15).
-// The row tiles take turns: while one's softmax runs, the tensor pipe has the other's
-// two products (PV of one key tile, S of the next).  P overlies S, so that the next S
-// waits for the product that reads P: the order of two tcgen05.mma with different
-// accumulators is not guaranteed otherwise.
+//   warp 20      issues S = Q K^T and O += P V (tcgen05.mma, M 128), 64 keys at a
+//                time, S and O in TMEM;
+//   warps 0-15   two threads per query row, 32 of the 64 keys each: running maximum,
+//                P = 2^(S - m) as fp16 over half of its S columns, running sum; O is
+//                rescaled only when a maximum grew by more than 2^8 (exact either way:
+//                m is any reference, and fp16 holds 2^15).
+// Of a row tile's two S buffers one is worked on while the next S is computed into the
+// other, once the product that read P there is done (the order of two tcgen05.mma with
+// different accumulators is not guaranteed otherwise).
 // Tiles use the canonical no-swizzle layouts, K as rows of channels (K-major), V as
 // stored (MN-major); the pipe runs them at its full rate (64 cycles an instruction).
 // Within 8 channels the order is 0 4 1 5 2 6 3 7, in which the nibbles of a word come
@@ -36,9 +35,10 @@ using namespace kie;
 
 namespace {
 
-constexpr int KEYS = 128;             // keys per tile
+constexpr int KEYS = 128;             // keys per K and V tile
+constexpr int STEP = 64;              // keys per S
 constexpr int ROWS = 256;             // query rows per CTA, in two tiles
-constexpr int THREADS = 640;
+constexpr int THREADS = 672;
 constexpr int WAIT_TRIES = 100000;    // of up to 20 us each: 2 s, then the rows become NaN
 constexpr float LAZY = 8.f;           // log2 of the growth of a maximum that is left alone
 constexpr float UP = 7.f;             // p is at most 2^(LAZY + UP): fp16's range
@@ -59,8 +59,9 @@ struct Sm {
     // never two CTAs on an SM: one takes all of TMEM
     static constexpr uint32_t BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
 };
-// [2]: per stage (K, V) or row tile (S, P, PV)
-enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 10, PVDONE = 12, FIN = 14, NBARS = 15 };
+// K, V: per stage; S, P: per row tile and buffer (each may be a step ahead of who waits
+// for it, and a barrier tells only two phases apart); PVDONE: per row tile.
+enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 12, PVDONE = 16, FIN = 18, NBARS = 19 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* failed) {
     for (int i = 0; i < WAIT_TRIES; ++i) {
@@ -109,10 +110,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
         ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 // 16 columns of this warp's TMEM lanes without waiting; and the wait for every load,
 // through which the registers go, so that no use of them moves before it.
@@ -222,18 +219,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[KFULL + i], 4);
-            mbar_init(&bar[KFREE + i], ntl);
+            mbar_init(&bar[KFREE + i], 1);
             mbar_init(&bar[VFULL + i], 4);
-            mbar_init(&bar[VFREE + i], ntl);
-            mbar_init(&bar[SFULL + i], 1);
-            mbar_init(&bar[PFULL + i], 8);
+            mbar_init(&bar[VFREE + i], 1);
             mbar_init(&bar[PVDONE + i], 1);
         }
-        mbar_init(&bar[FIN], ntl);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar[SFULL + i], 1);
+            mbar_init(&bar[PFULL + i], 8);
+        }
+        mbar_init(&bar[FIN], 1);
         *failed = 0;
         mbar_fence_init();
     }
-    if (warp == 16) tmem_alloc(taddr, 512);
+    if (warp == 20) tmem_alloc(taddr, 512);
 
     // ---- Q: a power of two brings a row's largest element to [1, 2)
     // softmax thread: row tile t, half h of the keys, row `lr` of the tile
@@ -287,7 +286,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
     const uint32_t tmem = *taddr;                  // S of the row tiles at 0 and 128, O at 256 and 384
 
     float m = -INFINITY, l = 0.f;
-    if (warp >= 16) {
+    auto ready = [&](int bi, uint32_t ph) { return !__any_sync(0xffffffffu, !wait_for(&bar[bi], ph, failed)); };
+    if (warp >= 16 && warp < 20) {
         // ---- codes to tiles: thread = key
         const int k = tid - 512;
         const size_t row0 = (size_t(b) * c.heads + head) * c.ctx_pad;
@@ -382,6 +382,68 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
             arrive(VFULL + (i & 1));
             if (i + 1 < ntile) load_v(i + 1);
         }
+    } else if (warp == 20) {
+        // ---- the tensor cores
+        const uint32_t el = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        constexpr uint32_t IS = (1u << 4) | (uint32_t(STEP >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+        constexpr uint32_t IO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+        constexpr uint32_t HALF = STEP / 8 * (L::SBO / 16);              // addresses in units of 16 bytes
+        const uint64_t dq = smem_desc_noswz(sm + L::Q, 128, L::SBO);
+        const uint64_t dk = smem_desc_noswz(sm + L::K, 128, L::SBO), dv = smem_desc_noswz(sm + L::V, L::SBO, 128);
+        const int nstep = 2 * ntile;
+        // S of row tile tl and step j (half j & 1 of key tile j / 2), into its buffer j & 1
+        auto issue_s = [&](int tl, int j) {
+            const int i = j >> 1;
+            if (!ready(KFULL + (i & 1), uint32_t(i >> 1) & 1u)) return false;
+            tc_fence_after();
+            const uint64_t q = dq + tl * (L::TILE / 16), k = dk + (i & 1) * (L::TILE / 16) + (j & 1) * HALF;
+            const uint32_t d = tm + tl * 128 + (j & 1) * STEP;
+            mma_ss<false>(d, q, k, IS, el);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk) mma_ss<true>(d, q + kk * 16, k + kk * 16, IS, el);
+            commit(&bar[SFULL + 2 * tl + (j & 1)], el);
+            if ((j & 1) && tl == ntl - 1) commit(&bar[KFREE + (i & 1)], el);
+            return true;
+        };
+        auto issue_pv = [&](int tl, int j) {
+            const int i = j >> 1;
+            const uint32_t ph = uint32_t(j) & 1u;
+            if (!ready(VFULL + (i & 1), uint32_t(i >> 1) & 1u) || !ready(PFULL + 2 * tl + (j & 1), uint32_t(j >> 1) & 1u)) return false;
+            tc_fence_after();
+            const uint64_t v = dv + (i & 1) * (L::TILE / 16) + (j & 1) * HALF;
+            const uint32_t p = tm + tl * 128 + ph * STEP, d = tm + 256 + tl * 128;
+            mma_ts(d, p, v, IO, j > 0 ? 1u : 0u, el);
+#pragma unroll
+            for (int kk = 1; kk < STEP / 16; ++kk)
+                mma_ts(d, p + (kk >> 1) * 32 + (kk & 1) * 8, v + kk * (2 * L::SBO / 16), IO, 1u, el);
+            commit(&bar[PVDONE + tl], el);
+            if ((j & 1) && tl == ntl - 1) commit(&bar[VFREE + (i & 1)], el);
+            return true;
+        };
+        // A row tile's next S but one goes into the buffer whose P its last product has
+        // read; with two row tiles the other one's work lies between the two.
+        bool ok = ntile == 0 || issue_s(0, 0);
+        if (ntl == 2) {
+            ok = ok && (ntile == 0 || (issue_s(1, 0) && issue_s(0, 1)));
+            for (int j = 0; ok && j < nstep; ++j) {
+                const uint32_t ph = uint32_t(j) & 1u;
+                ok = issue_pv(0, j);
+                if (ok && j + 1 < nstep) ok = (j == 0 || ready(PVDONE + 1, ph ^ 1u)) && issue_s(1, j + 1);
+                ok = ok && issue_pv(1, j);
+                if (ok && j + 2 < nstep) ok = ready(PVDONE, ph) && issue_s(0, j + 2);
+            }
+        } else {
+            ok = ok && (ntile == 0 || issue_s(0, 1));
+            for (int j = 0; ok && j < nstep; ++j) {
+                ok = issue_pv(0, j);
+                if (ok && j + 2 < nstep) ok = ready(PVDONE, uint32_t(j) & 1u) && issue_s(0, j + 2);
+            }
+        }
+        // everything issued has landed before the accumulators are read or given back
+        commit(&bar[FIN], el);
+        wait_for(&bar[FIN], 0u, failed);
+        __syncwarp();
     } else if (t < ntl) {
         // ---- softmax: threads (t, 0, lr) and (t, 1, lr) share a row
         const uint32_t my = tmem + (uint32_t((warp & 3) * 32) << 16);       // this warp's TMEM lanes
@@ -390,66 +452,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
         const int firstk = A.a.window > 0 ? last - A.a.window + 1 : 0;
         const int all_lo = __reduce_max_sync(0xffffffffu, have ? firstk : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, have ? last : 1 << 30);
-        // the row tile's products: its first warp issues
-        const bool issuer = (warp & 7) == 0;
-        const uint32_t el = elect_one();
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        constexpr uint32_t IS = (1u << 4) | (uint32_t(KEYS >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-        constexpr uint32_t IO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-        // addresses in units of 16 bytes
-        const uint64_t dq = smem_desc_noswz(sm + L::Q, 128, L::SBO) + t * (L::TILE / 16);
-        const uint64_t dk = smem_desc_noswz(sm + L::K, 128, L::SBO), dv = smem_desc_noswz(sm + L::V, L::SBO, 128);
-        auto ready = [&](int bi, uint32_t ph) { return !__any_sync(0xffffffffu, !wait_for(&bar[bi], ph, failed)); };
-        auto issue_s = [&](int i) {
-            if (!ready(KFULL + (i & 1), uint32_t(i >> 1) & 1u)) return false;
+        const int nstep = 2 * ntile;
+        for (int j = 0; j < nstep; ++j) {
+            const uint32_t ph = uint32_t(j) & 1u;
+            if (!ready(SFULL + 2 * t + (j & 1), uint32_t(j >> 1) & 1u)) break;
             tc_fence_after();
-            const uint64_t k = dk + (i & 1) * (L::TILE / 16);
-            mma_ss<false>(tm + t * 128, dq, k, IS, el);
+            const int p0 = base + j * STEP + h * 32;
+            const uint32_t th = ts + ph * STEP + h * 32;       // this half's columns: S, then P over the first 16
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(th, s);
+            if (p0 < all_lo || p0 + 31 > all_hi) {             // uniform over the warp
+                const int f = firstk - p0, e1 = last - p0;     // columns f .. e1 are seen
 #pragma unroll
-            for (int kk = 1; kk < D / 16; ++kk) mma_ss<true>(tm + t * 128, dq + kk * 16, k + kk * 16, IS, el);
-            commit(&bar[SFULL + t], el);
-            commit(&bar[KFREE + (i & 1)], el);
-            return true;
-        };
-        // the second row tile starts when the first has its P, so that they take turns
-        if (issuer && ntile > 0 && (t == 0 || ready(PFULL, 0u))) issue_s(0);
-        for (int i = 0; i < ntile; ++i) {
-            const uint32_t ph = uint32_t(i) & 1u;
-            if (__any_sync(0xffffffffu, !wait_for(&bar[SFULL + t], ph, failed))) break;
-            tc_fence_after();
-            const int p0 = base + i * KEYS + h * 64;
-            const bool edge = p0 < all_lo || p0 + 63 > all_hi;          // uniform over the warp
-            const uint32_t th = ts + h * 64;       // this half's columns: S, then P over the first 32
-            float mt = -INFINITY;
-            if (edge) {                            // mask S in place
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t s[16];
-                    tmem_ld_x16(th + q * 16, s);
-                    tmem_wait_ld(s);
-                    const int f = firstk - p0 - q * 16, e1 = last - p0 - q * 16;  // columns f .. e1 are seen
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (e < f || e > e1) s[e] = 0xFF800000u;
-                    tmem_st_x16(th + q * 16, s);
-                }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                for (int e = 0; e < 32; ++e)
+                    if (e < f || e > e1) s[e] = 0xFF800000u;
             }
-            uint32_t s[2][16];                     // the next 16 columns land while these are worked on
-            tmem_ld_x16(th, s[0]);
+            float a[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                tmem_wait_ld(s[q & 1]);
-                if (q < 3) tmem_ld_x16(th + (q + 1) * 16, s[(q + 1) & 1]);
-                float a[2] = {-INFINITY, -INFINITY};
+            for (int e = 0; e < 32; e += 4)
 #pragma unroll
-                for (int e = 0; e < 16; e += 4)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        a[j] = max3_nan(a[j], __uint_as_float(s[q & 1][e + 2 * j]), __uint_as_float(s[q & 1][e + 2 * j + 1]));
-                mt = max3_nan(mt, a[0], a[1]);
-            }
-            mt *= cq;
+                for (int q = 0; q < 2; ++q) a[q] = max3_nan(a[q], __uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
+            float mt = max_nan(a[0], a[1]) * cq;
             float* mx = maxes + ((ph * 2 + t) * 2) * 128 + lr;
             mx[h * 128] = mt;
             asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");
@@ -460,59 +483,38 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
                 l *= f;
                 m = mt;
             }
-            if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {       // the last product is done: this S was issued after it
+            if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                if (!ready(PVDONE + t, ph ^ 1u)) break;
+                tc_fence_after();
 #pragma unroll 1
-                for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(to + c0, o);
+                for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 16) {
+                    uint32_t o[16];
+                    tmem_ld_x16(to + c0, o);
+                    tmem_wait_ld(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st_32x32b_x32(to + c0, o);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st_x16(to + c0, o);
                 }
             }
             const float ref = (m == -INFINITY ? 0.f : m) - UP;
             float2 sum = make_float2(0.f, 0.f), sum2 = sum;
-            tmem_ld_x16(th, s[0]);                 // again, for P
+            uint32_t hp[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                tmem_wait_ld(s[q & 1]);
-                if (q < 3) tmem_ld_x16(th + (q + 1) * 16, s[(q + 1) & 1]);
-                uint32_t hp[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1])),
-                                                make_float2(cq, cq), make_float2(-ref, -ref));
-                    const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                    if (e & 1) sum = __fadd2_rn(sum, p);
-                    else sum2 = __fadd2_rn(sum2, p);
-                    hp[e] = pack_h2(p.x, p.y);
-                }
-                tmem_st_x8(th + q * 8, hp);        // over columns that are read already
+            for (int e = 0; e < 16; ++e) {
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                            make_float2(cq, cq), make_float2(-ref, -ref));
+                const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                if (e & 1) sum = __fadd2_rn(sum, p);
+                else sum2 = __fadd2_rn(sum2, p);
+                hp[e] = pack_h2(p.x, p.y);
             }
+            tmem_st_x16(th, hp);
             l += (sum.x + sum.y) + (sum2.x + sum2.y);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[PFULL + t]);
-            if (issuer) {
-                if (!ready(VFULL + (i & 1), uint32_t(i >> 1) & 1u) || !ready(PFULL + t, ph)) break;
-                tc_fence_after();
-                const uint64_t v = dv + (i & 1) * (L::TILE / 16);
-                mma_ts(tm + 256 + t * 128, tm + t * 128, v, IO, i > 0 ? 1u : 0u, el);
-#pragma unroll
-                for (int kk = 1; kk < KEYS / 16; ++kk)
-                    mma_ts(tm + 256 + t * 128, tm + t * 128 + (kk >> 2) * 64 + (kk & 3) * 8, v + kk * (2 * L::SBO / 16), IO, 1u, el);
-                commit(&bar[PVDONE + t], el);
-                commit(&bar[VFREE + (i & 1)], el);
-                if (i + 1 < ntile && !(ready(PVDONE + t, ph) && issue_s(i + 1))) break;
-            }
+            if (lane == 0) mbar_arrive(&bar[PFULL + 2 * t + (j & 1)]);
         }
-        // everything issued has landed before the accumulators are read or given back
-        if (issuer) {
-            commit(&bar[FIN], el);
-            wait_for(&bar[FIN], 0u, failed);
-        }
-        __syncwarp();
         sums[(t * 2 + h) * 128 + lr] = l;
     }
     __syncthreads();
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) tmem_dealloc(tmem, 512);
+    if (warp == 20) tmem_dealloc(tmem, 512);
 }
 
 // Join the stretches of the keys.  One block per item and 2 rows (D = 128) or 4.

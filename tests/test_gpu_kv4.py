@@ -297,3 +297,25 @@ def test_calls_on_two_streams():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dim,group,heads,kv_heads,n_q,window", [(128, 64, 4, 4, 300, 0), (64, 32, 8, 2, 129, 0),
+                                                                (128, 128, 2, 1, 200, 900), (64, 64, 16, 1, 33, 0),
+                                                                (128, 32, 4, 2, 128, 0)])
+def test_many_tokens_over_a_long_cache(dim, group, heads, kv_heads, n_q, window):
+    """Many key tiles per row tile, one and two row tiles, the keys split over CTAs."""
+    lens, news = [5000, 2977], [n_q, n_q - 1]
+    cache, k, v = filled(2, kv_heads, 5000, dim, group, lens)
+    q = gen((2, n_q, heads, dim), 61, "bf16", std=1.5, outliers=False)
+    out = cache.attention(q, i32(*lens), n_tok=i32(*news), window=window)
+    rows = [0, 1, n_q // 2, n_q - 2]                      # a few rows of each request against 64 bits
+    for b in range(2):
+        for t in rows:
+            if t >= news[b]:
+                continue
+            n = lens[b] - news[b] + t + 1
+            check(out[b:b + 1, t:t + 1], q[b:b + 1, t:t + 1], k[b:b + 1, :n], v[b:b + 1, :n], [n], [1], "bf16",
+                  window=window)
+    assert torch.isfinite(out[0]).all()
+    again = cache.attention(q, i32(*lens), n_tok=i32(*news), window=window)
+    assert torch.equal(out[0], again[0])
