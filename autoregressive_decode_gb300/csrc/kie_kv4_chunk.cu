@@ -64,6 +64,7 @@ struct Sm {
 enum { KFULL = 0, KFREE = 2, VFULL = 4, VFREE = 6, SFULL = 8, PFULL = 12, PVDONE = 16, FIN = 18, NBARS = 19 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* failed) {
+#pragma unroll 1
     for (int i = 0; i < WAIT_TRIES; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15) == 15 && *failed) return false;
@@ -80,21 +81,24 @@ __device__ __forceinline__ uint32_t elect_one() {
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
     return p;
 }
-// D[tmem] (+)= A B^T, A and B from shared memory.
+// D[tmem] (+)= A B^T, A and B from shared memory; descriptors by their low words and a
+// common high one.
 template <bool ACC>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t el) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t el) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(el), "n"(ACC ? 1 : 0)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(el), "n"(ACC ? 1 : 0)
         : "memory");
 }
 // A (P, fp16 pairs in 32-bit columns) from TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t el) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t el) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(el)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 q, %6, 0;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(el)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar, uint32_t el) {
@@ -388,56 +392,73 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         constexpr uint32_t IS = (1u << 4) | (uint32_t(STEP >> 3) << 17) | (uint32_t(128 >> 4) << 24);
         constexpr uint32_t IO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-        constexpr uint32_t HALF = STEP / 8 * (L::SBO / 16);              // addresses in units of 16 bytes
+        constexpr uint32_t HALF = STEP / 8 * (L::SBO / 16), STAGE = L::TILE / 16;       // addresses in units of 16 bytes
         const uint64_t dq = smem_desc_noswz(sm + L::Q, 128, L::SBO);
         const uint64_t dk = smem_desc_noswz(sm + L::K, 128, L::SBO), dv = smem_desc_noswz(sm + L::V, L::SBO, 128);
-        const int nstep = 2 * ntile;
-        // S of row tile tl and step j (half j & 1 of key tile j / 2), into its buffer j & 1
-        auto issue_s = [&](int tl, int j) {
-            const int i = j >> 1;
-            if (!ready(KFULL + (i & 1), uint32_t(i >> 1) & 1u)) return false;
-            tc_fence_after();
-            const uint64_t q = dq + tl * (L::TILE / 16), k = dk + (i & 1) * (L::TILE / 16) + (j & 1) * HALF;
-            const uint32_t d = tm + tl * 128 + (j & 1) * STEP;
-            mma_ss<false>(d, q, k, IS, el);
-#pragma unroll
-            for (int kk = 1; kk < D / 16; ++kk) mma_ss<true>(d, q + kk * 16, k + kk * 16, IS, el);
-            commit(&bar[SFULL + 2 * tl + (j & 1)], el);
-            if ((j & 1) && tl == ntl - 1) commit(&bar[KFREE + (i & 1)], el);
-            return true;
+        // Nothing here branches on what one thread alone knows: a wait that runs out leaves
+        // its mark in `failed` and the work goes on with what is there (the rows become NaN),
+        // so that loops, descriptors and addresses stay in the uniform registers.
+        const int nstep = __shfl_sync(0xffffffffu, 2 * ntile, 0), nt2 = __shfl_sync(0xffffffffu, ntl, 0);
+        const uint32_t qlo = uint32_t(dq), klo = uint32_t(dk), vlo = uint32_t(dv);
+        const uint32_t qhi = uint32_t(dq >> 32), vhi = uint32_t(dv >> 32);      // K's is Q's
+        auto wait = [&](int bi, uint32_t parity) {
+            wait_for(&bar[bi], parity, failed);
+            __syncwarp();
         };
-        auto issue_pv = [&](int tl, int j) {
-            const int i = j >> 1;
-            const uint32_t ph = uint32_t(j) & 1u;
-            if (!ready(VFULL + (i & 1), uint32_t(i >> 1) & 1u) || !ready(PFULL + 2 * tl + (j & 1), uint32_t(j >> 1) & 1u)) return false;
+        // Steps j = 4 n + q: q alone gives the stage (q >> 1), the half of the key tile and
+        // the S buffer (q & 1) and the parities of a buffer's and of a row tile's barriers;
+        // `par` is that of the stages' barriers for n.  S of row tile tl and step q (up to
+        // two steps ahead, q < 6):
+        auto issue_s = [&](int tl, int q, uint32_t par) {
+            if (tl == 0 && (q & 1) == 0) wait(KFULL + ((q >> 1) & 1), par ^ uint32_t(q >> 2));
             tc_fence_after();
-            const uint64_t v = dv + (i & 1) * (L::TILE / 16) + (j & 1) * HALF;
-            const uint32_t p = tm + tl * 128 + ph * STEP, d = tm + 256 + tl * 128;
-            mma_ts(d, p, v, IO, j > 0 ? 1u : 0u, el);
+            const uint32_t a = qlo + tl * STAGE, k = klo + ((q >> 1) & 1) * STAGE + (q & 1) * HALF;
+            const uint32_t d = tm + tl * 128 + (q & 1) * STEP;
+            mma_ss<false>(d, a, k, qhi, IS, el);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk) mma_ss<true>(d, a + kk * 16, k + kk * 16, qhi, IS, el);
+            commit(&bar[SFULL + 2 * tl + (q & 1)], el);
+            if ((q & 1) && tl == nt2 - 1) commit(&bar[KFREE + ((q >> 1) & 1)], el);
+        };
+        auto issue_pv = [&](int tl, int q, uint32_t par, uint32_t accumulate) {
+            if (tl == 0 && (q & 1) == 0) wait(VFULL + ((q >> 1) & 1), par);
+            wait(PFULL + 2 * tl + (q & 1), uint32_t(q >> 1) & 1u);
+            tc_fence_after();
+            const uint32_t v = vlo + ((q >> 1) & 1) * STAGE + (q & 1) * HALF;
+            const uint32_t p = tm + tl * 128 + (q & 1) * STEP, d = tm + 256 + tl * 128;
+            mma_ts(d, p, v, vhi, IO, accumulate, el);
 #pragma unroll
             for (int kk = 1; kk < STEP / 16; ++kk)
-                mma_ts(d, p + (kk >> 1) * 32 + (kk & 1) * 8, v + kk * (2 * L::SBO / 16), IO, 1u, el);
+                mma_ts(d, p + (kk >> 1) * 32 + (kk & 1) * 8, v + kk * (2 * L::SBO / 16), vhi, IO, 1u, el);
             commit(&bar[PVDONE + tl], el);
-            if ((j & 1) && tl == ntl - 1) commit(&bar[VFREE + (i & 1)], el);
-            return true;
+            if ((q & 1) && tl == nt2 - 1) commit(&bar[VFREE + ((q >> 1) & 1)], el);
         };
         // A row tile's next S but one goes into the buffer whose P its last product has
         // read; with two row tiles the other one's work lies between the two.
-        bool ok = ntile == 0 || issue_s(0, 0);
-        if (ntl == 2) {
-            ok = ok && (ntile == 0 || (issue_s(1, 0) && issue_s(0, 1)));
-            for (int j = 0; ok && j < nstep; ++j) {
-                const uint32_t ph = uint32_t(j) & 1u;
-                ok = issue_pv(0, j);
-                if (ok && j + 1 < nstep) ok = (j == 0 || ready(PVDONE + 1, ph ^ 1u)) && issue_s(1, j + 1);
-                ok = ok && issue_pv(1, j);
-                if (ok && j + 2 < nstep) ok = ready(PVDONE, ph) && issue_s(0, j + 2);
-            }
-        } else {
-            ok = ok && (ntile == 0 || issue_s(0, 1));
-            for (int j = 0; ok && j < nstep; ++j) {
-                ok = issue_pv(0, j);
-                if (ok && j + 2 < nstep) ok = ready(PVDONE, uint32_t(j) & 1u) && issue_s(0, j + 2);
+        if (nstep > 0) {
+            issue_s(0, 0, 0u);
+            if (nt2 == 2) issue_s(1, 0, 0u);
+            issue_s(0, 1, 0u);
+        }
+#pragma unroll 1
+        for (int j0 = 0; j0 < nstep; j0 += 4) {
+            const uint32_t par = uint32_t(j0 >> 2) & 1u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = j0 + q;
+                if (j >= nstep) break;
+                issue_pv(0, q, par, j > 0 ? 1u : 0u);
+                if (nt2 == 2) {
+                    if (j + 1 < nstep) {
+                        if (j > 0) wait(PVDONE + 1, uint32_t(q & 1) ^ 1u);
+                        issue_s(1, q + 1, par);
+                    }
+                    issue_pv(1, q, par, j > 0 ? 1u : 0u);
+                }
+                if (j + 2 < nstep) {
+                    wait(PVDONE, uint32_t(q & 1));
+                    issue_s(0, q + 2, par);
+                }
             }
         }
         // everything issued has landed before the accumulators are read or given back
