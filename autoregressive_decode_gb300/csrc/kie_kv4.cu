@@ -1093,7 +1093,7 @@ cudaError_t opt_in(K* kernel, int bytes, std::atomic<uint64_t>& done) {
 // How an attention runs, by what the host knows: the mode, the row tiles and the form.
 struct Plan {
     int mode, per, nrt, nctas;
-    int64_t items;
+    int64_t items, tiles;    // tiles: the most that an item can have
     int S;                   // CTAs per item of the cluster form; 0: stream form
 };
 Plan plan_of(const Kv4Attn& a, int sms) {
@@ -1105,24 +1105,32 @@ Plan plan_of(const Kv4Attn& a, int sms) {
     p.nrt = int((rows + rt - 1) / rt);
     p.nctas = sms * ctas_per_sm(p.mode, a.c.dim);
     p.items = int64_t(a.c.batch) * p.nrt * a.c.heads;
-    // the most tiles an item can have
     int64_t keys = a.c.max_ctx;
     if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + (rt + p.per - 1) / p.per + TP);
-    const int64_t tiles = (keys + TP - 1) / TP;
+    const int64_t tiles = p.tiles = (keys + TP - 1) / TP;
     // Cluster form while a warp has few tiles: there the second launch and the list's
     // set-up cost more than an uneven split.  2,300 keys x 16 heads: 10.1 us against
     // 12.6 in the stream form; 32,768 x 16: 43 against 25.
     p.S = 0;
     if (p.items * tiles <= int64_t(p.nctas) * NW * 4) {
         p.S = 1;
-        while (p.S < MAXS && p.S * NW < tiles && p.items * p.S * 2 <= p.nctas) p.S *= 2;
+        // clusters of 8 fill 120 of the 152 SMs with one CTA each, 288 of 304 with two
+        const int64_t room = p.nctas == sms ? p.nctas * 3 / 4 : p.nctas * 15 / 16;
+        while (p.S < MAXS && p.S * NW < tiles && p.items * p.S * 2 <= room) p.S *= 2;
     }
     return p;
 }
 
-// Whether the kernel of 128-row tiles takes the call.
-bool many_tokens(const Kv4Attn& a) {
-    return a.type == KV4_BF16 && int64_t(a.n_q) * (a.heads / a.c.heads) >= 64;
+// Whether the kernel of 256-row tiles (kie_kv4_chunk.cu) takes the call: where its
+// modelled time is the smaller, from the same bound on the keys.  Here a 16-row, 32-key
+// unit takes 1.75 ns of the whole GPU after 6 us.  Measured at 128 channels, group 64
+// (rows: this / that): 8 x 16 heads over 4,096 keys 16: 37 / 53 us, 64: 113 / 53; 8 heads
+// over 32,768 keys 32: 33 / 38, 128: 83 / 45; 8 heads over 4,096 keys 64: 13 / 22, 512:
+// 60 / 45.
+bool many_tokens(const Kv4Attn& a, int sms) {
+    if (a.type != KV4_BF16 || int64_t(a.n_q) * (a.heads / a.c.heads) <= 16) return false;
+    const Plan p = plan_of(a, sms);
+    return 6.0 + 1.75e-3 * double(p.items) * double(p.tiles) * a.c.dim / 128 > kie_kv4_chunk_us(&a, sms);
 }
 
 template <int D, int NG, int MODE, int T>
@@ -1217,13 +1225,13 @@ extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const
 // i: a CTA's items and an item's CTAs are both consecutive, so no two (item, CTA)
 // pairs that meet share a slot.  The cluster form needs none.
 extern "C" size_t kie_kv4_attention_ws_floats(const Kv4Attn* a, int sms) {
-    if (many_tokens(*a)) return kie_kv4_chunk_ws_floats(a, sms);
+    if (many_tokens(*a, sms)) return kie_kv4_chunk_ws_floats(a, sms);
     const Plan p = plan_of(*a, sms);
     return p.S ? 0 : size_t(p.items + p.nctas) * rows_of(p.mode) * (a->c.dim + 2);
 }
 
 extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaStream_t st) {
-    if (many_tokens(*a)) return kie_launch_kv4_chunk(a, sms, st);
+    if (many_tokens(*a, sms)) return kie_launch_kv4_chunk(a, sms, st);
     const Plan p = plan_of(*a, sms);
     const AttnArgs A{*a, p.per, p.nrt, p.nctas};
     const int ng = a->c.dim / a->c.group;

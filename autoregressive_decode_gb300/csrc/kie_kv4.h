@@ -65,6 +65,7 @@ extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const
 extern "C" size_t kie_kv4_attention_ws_floats(const Kv4Attn* a, int sms);
 extern "C" cudaError_t kie_launch_kv4_attention(const Kv4Attn* a, int sms, cudaStream_t st);
 
-// The same for many tokens of bf16 (kie_kv4_chunk.cu).
+// The same for many tokens of bf16 (kie_kv4_chunk.cu), and a model of its time.
+extern "C" double kie_kv4_chunk_us(const Kv4Attn* a, int sms);
 extern "C" size_t kie_kv4_chunk_ws_floats(const Kv4Attn* a, int sms);
 extern "C" cudaError_t kie_launch_kv4_chunk(const Kv4Attn* a, int sms, cudaStream_t st);

@@ -635,7 +635,7 @@ cudaError_t launch(const ChunkArgs& A, int items, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-struct ChunkPlan { int per, nrt, nsplit; int64_t items; };
+struct ChunkPlan { int per, nrt, nsplit; int64_t items, tiles; };
 ChunkPlan plan_of(const Kv4Attn& a, int sms) {
     ChunkPlan p;
     p.per = a.heads / a.c.heads;
@@ -643,13 +643,22 @@ ChunkPlan plan_of(const Kv4Attn& a, int sms) {
     p.items = int64_t(p.nrt) * a.c.batch * a.c.heads;
     int64_t keys = a.c.max_ctx;
     if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + ROWS / p.per + 1);
-    const int64_t tiles = (keys + KEYS - 1) / KEYS + (a.window > 0);
-    // stretches of at least four tiles while SMs are left over
-    p.nsplit = int(std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(p.items, 1), tiles / 4)));
+    p.tiles = (keys + KEYS - 1) / KEYS + (a.window > 0);
+    // stretches of at least two tiles while SMs are left over
+    p.nsplit = int(std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(p.items, 1), p.tiles / 2)));
     return p;
 }
 
 }  // namespace
+
+// 18 us of set-up, 2.2 us per key tile and round of CTAs (1.1 with one row tile), 0.5 us
+// per stretch to join; 64 channels take about 0.7 of that.
+extern "C" double kie_kv4_chunk_us(const Kv4Attn* a, int sms) {
+    const ChunkPlan p = plan_of(*a, sms);
+    const bool one = int64_t(a->n_q) * p.per <= 128;
+    const double rounds = double((p.items * p.nsplit + sms - 1) / sms), tiles = double((p.tiles + p.nsplit - 1) / p.nsplit);
+    return 18.0 + rounds * tiles * (one ? 1.1 : 2.2) * (a->c.dim == 64 ? 0.7 : 1.0) + (p.nsplit > 1 ? 0.5 * p.nsplit : 0.0);
+}
 
 extern "C" size_t kie_kv4_chunk_ws_floats(const Kv4Attn* a, int sms) {
     const ChunkPlan p = plan_of(*a, sms);
