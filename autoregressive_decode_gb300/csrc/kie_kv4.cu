@@ -120,24 +120,35 @@ struct RowArgs {
     Kv4Strides ks, vs;
     const int32_t *start, *n_tok;
     int32_t n, chunks;       // tokens, blocks per request
+    int32_t dt, dh;          // (256 / lanes per row) / heads and its remainder: from a thread's row to its next
 };
 
-// This thread's k-th row: its token and head, and where it is stored (false: nowhere).
-struct Place { int b, t, h; size_t row; };
+// A block's request, its tokens and first position; a thread's row: token and head.
+struct Where { int b, nt, t, h; int64_t start; };
 template <int D>
-__device__ __forceinline__ bool place(const RowArgs& A, int k, Place& p) {
-    p.b = int(blockIdx.x) / A.chunks;
-    const int first = (int(blockIdx.x) - p.b * A.chunks) * rows_per_block<D>();
-    const int r = first + k * (256 / (D / 8)) + threadIdx.x / (D / 8);
-    p.t = r / A.c.heads;
-    p.h = r - p.t * A.c.heads;
-    const int nt = A.n_tok ? min(__ldg(A.n_tok + p.b), A.n) : A.n;
-    const int64_t pos = int64_t(__ldg(A.start + p.b)) + p.t;
-    p.row = (size_t(p.b) * A.c.heads + p.h) * A.c.ctx_pad + size_t(pos);
-    return p.t < nt && pos >= 0 && pos < A.c.max_ctx;
+__device__ __forceinline__ Where where(const RowArgs& A) {
+    Where w;
+    w.b = int(blockIdx.x) / A.chunks;
+    const int r = (int(blockIdx.x) - w.b * A.chunks) * rows_per_block<D>() + threadIdx.x / (D / 8);
+    w.t = r / A.c.heads;
+    w.h = r - w.t * A.c.heads;
+    w.nt = A.n_tok ? min(__ldg(A.n_tok + w.b), A.n) : A.n;
+    w.start = __ldg(A.start + w.b);
+    return w;
+}
+// Row of the codes at which the current token is stored; false: it is not.
+__device__ __forceinline__ bool stored_at(const RowArgs& A, const Where& w, size_t& row) {
+    const int64_t pos = w.start + w.t;
+    row = (size_t(w.b) * A.c.heads + w.h) * A.c.ctx_pad + size_t(pos);
+    return w.t < w.nt && pos >= 0 && pos < A.c.max_ctx;
+}
+__device__ __forceinline__ void next_row(const RowArgs& A, Where& w) {
+    w.t += A.dt;
+    w.h += A.dh;
+    if (w.h >= A.c.heads) { w.h -= A.c.heads; ++w.t; }
 }
 
-// Eight channels as fp16 pairs, saturated to +-65504, NaN as 0.
+// Eight channels as fp16 pairs (not yet saturated).
 template <int T>
 __device__ __forceinline__ void load_h2(const typename Elem<T>::type* p, __half2* x) {
     if (T == KV4_F16 && aligned16(p)) {
@@ -150,76 +161,89 @@ __device__ __forceinline__ void load_h2(const typename Elem<T>::type* p, __half2
     }
 }
 
-template <int T, int D>
+// d / 15, rounded to nearest even: with y = RN(1/15) and q = RN(d y), within an ulp of the
+// quotient, the residual d - 15 q is exact and RN(q + residual y) is RN(d / 15) (P.
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990).  d is a difference of fp16 values: no underflow.
+__device__ __forceinline__ float div15(float d) {
+    constexpr float Y = 1.f / 15.f;
+    const float q = d * Y;
+    return fmaf(fmaf(-15.f, q, d), Y, q);
+}
+
+template <int T, int D, int NG>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const RowArgs A, const void* k, const void* v) {
     using E = typename Elem<T>::type;
-    constexpr int LPR = D / 8, BLK = D / 32;
+    constexpr int LPR = D / 8, BLK = D / 32, LPG = LPR / NG;      // lanes per row, blocks, lanes per group
     const int lane = threadIdx.x & 31, l = lane % LPR;
     const bool isv = blockIdx.y != 0;
     const Kv4& c = A.c;
     const Kv4Strides& s = isv ? A.vs : A.ks;
-    const int ng = D / c.group, lpg = c.group / 8;
-    Place p[RPT];
+    Where w = where<D>(A);
+    size_t row[RPT];
     bool ok[RPT];
     __half2 x[RPT][4];
+    const E* base = static_cast<const E*>(isv ? v : k) + w.b * s.b + l * 8;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-        ok[u] = place<D>(A, u, p[u]);
+        ok[u] = stored_at(A, w, row[u]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[u][i] = __half2half2(__ushort_as_half(0));
-        if (ok[u]) load_h2<T>(static_cast<const E*>(isv ? v : k) + p[u].b * s.b + p[u].t * s.t + p[u].h * s.h + l * 8, x[u]);
+        if (ok[u]) load_h2<T>(base + w.t * s.t + w.h * s.h, x[u]);
+        next_row(A, w);
     }
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
         if (!__any_sync(0xffffffffu, ok[u])) continue;
-        const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), bottom = __hneg2(top);
+        // saturated to +-65504, NaN as 0
+        const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), bottom = __half2half2(__ushort_as_half(0xFBFF));
         __half2 lo2 = top, hi2 = bottom;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t num = __heq2_mask(x[u][i], x[u][i]);           // 0 where NaN
-            uint32_t w = *reinterpret_cast<uint32_t*>(&x[u][i]) & num;
-            x[u][i] = __hmax2(__hmin2(*reinterpret_cast<__half2*>(&w), top), bottom);
+            uint32_t bits = *reinterpret_cast<uint32_t*>(&x[u][i]) & __heq2_mask(x[u][i], x[u][i]);
+            x[u][i] = __hmax2(__hmin2(*reinterpret_cast<__half2*>(&bits), top), bottom);
             lo2 = __hmin2(lo2, x[u][i]);
             hi2 = __hmax2(hi2, x[u][i]);
         }
         // (minimum, -maximum) of the lane, then of the group: one exchange per step
-        __half2 mm = __halves2half2(__hmin(__low2half(lo2), __high2half(lo2)), __hneg(__hmax(__low2half(hi2), __high2half(hi2))));
-        for (int o = 1; o < lpg; o <<= 1) mm = __hmin2(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        __half2 mm = __hmin2(__lows2half2(lo2, __hneg2(hi2)), __highs2half2(lo2, __hneg2(hi2)));
+#pragma unroll
+        for (int o = 1; o < LPG; o <<= 1) mm = __hmin2(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         const float lo = __low2float(mm), hi = -__high2float(mm);
-        const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+        const __half sh = __float2half_rn(div15(hi - lo));
         const float sf = __half2float(sh);
-        const float rcp = sf > 0.f ? __frcp_rn(sf) : 0.f;
-        // code = rint((x - z) / s), at most 15: by the reciprocal, which is within 2^-19 of
+        float rcp;                   // 0 for a constant group: all codes 0
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(sf));
+        if (!(sf > 0.f)) rcp = 0.f;
+        // code = rint((x - z) / s), at most 15: by the reciprocal, which is within 2^-18 of
         // the quotient, so only a value that close to a half needs the division itself.
         // Adding 1.5 * 2^23 rounds to even and leaves the code in the low bits.
         constexpr float MAGIC = 12582912.f;
-        float d[8], c8[8];
-        bool close = false;
+        float d[8], c8[8], far = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             d[i] = (i & 1 ? __high2float(x[u][i >> 1]) : __low2float(x[u][i >> 1])) - lo;
-            const float q = d[i] * rcp;
-            c8[i] = q + MAGIC;
-            close |= fabsf(q - (c8[i] - MAGIC)) > 0.5f - 1.f / 65536.f;
+            c8[i] = fmaf(d[i], rcp, MAGIC);
+            far = fmaxf(far, fabsf(fmaf(d[i], rcp, -(c8[i] - MAGIC))));     // largest distance from a code
         }
-        if (close && sf > 0.f) {
+        if (far > 0.5f - 1.f / 65536.f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) c8[i] = rintf(__fdiv_rn(d[i], sf)) + MAGIC;
         }
-        uint32_t w = 0;
+        uint32_t word = 0;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) w = w * 16u + (__float_as_uint(fminf(c8[i], MAGIC + 15.f)) & 15u);
+        for (int i = 7; i >= 0; --i) word = word * 16u + (__float_as_uint(fminf(c8[i], MAGIC + 15.f)) & 15u);
         if (!isv) {
-            if (ok[u]) reinterpret_cast<uint32_t*>(c.kc)[p[u].row * LPR + (l & 3) * BLK + (l >> 2)] = w;
+            if (ok[u]) reinterpret_cast<uint32_t*>(c.kc)[row[u] * LPR + (l & 3) * BLK + (l >> 2)] = word;
         } else {
             // lane l stores word l = units (g, 2wi) and (g, 2wi + 1): see kie_kv4.h
             const int g = l / (D / 64), wi = l % (D / 64);
             const int src = (lane - l) + 8 * wi + (g >> 1);
-            const uint32_t w0 = __shfl_sync(0xffffffffu, w, src), w1 = __shfl_sync(0xffffffffu, w, src + 4);
-            if (ok[u]) reinterpret_cast<uint32_t*>(c.vc)[p[u].row * LPR + l] = __byte_perm(w0, w1, (g & 1) ? 0x7632 : 0x5410);
+            const uint32_t w0 = __shfl_sync(0xffffffffu, word, src), w1 = __shfl_sync(0xffffffffu, word, src + 4);
+            if (ok[u]) reinterpret_cast<uint32_t*>(c.vc)[row[u] * LPR + l] = __byte_perm(w0, w1, (g & 1) ? 0x7632 : 0x5410);
         }
-        if (ok[u] && l % lpg == 0) {
-            const ParAt at = par_at(p[u].row, l / lpg, ng, isv);
+        if (ok[u] && l % LPG == 0) {
+            const ParAt at = par_at(row[u], l / LPG, NG, isv);
             uint16_t* pp = isv ? c.vp : c.kp;
             pp[at.s] = __half_as_ushort(sh);
             pp[at.z] = __half_as_ushort(__low2half(mm));
@@ -227,48 +251,59 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const RowArgs A, const 
     }
 }
 
-template <int T, int D>
+template <int T, int D, int NG>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k, void* v) {
     using E = typename Elem<T>::type;
-    constexpr int LPR = D / 8, BLK = D / 32;
+    constexpr int LPR = D / 8, BLK = D / 32, LPG = LPR / NG;
     const int l = threadIdx.x % LPR;
     const bool isv = blockIdx.y != 0;
     const Kv4& c = A.c;
     const Kv4Strides& st = isv ? A.vs : A.ks;
-    const int ng = D / c.group, gi = l * 8 / c.group;
-    Place p[RPT];
+    Where w = where<D>(A);
     bool ok[RPT];
-    uint32_t w[RPT];
-    uint16_t sz[RPT][2];
+    uint32_t word[RPT], sz[RPT];
+    const Where w0 = w;
+    const uint32_t* kc = reinterpret_cast<const uint32_t*>(c.kc) + (l & 3) * BLK + (l >> 2);
+    const uint16_t* vc = reinterpret_cast<const uint16_t*>(c.vc) + (2 * (l & 3)) * BLK + (l >> 2);
+    const uint16_t* pp = isv ? c.vp : c.kp;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-        ok[u] = place<D>(A, u, p[u]);
+        size_t row;
+        ok[u] = stored_at(A, w, row);
+        next_row(A, w);
         if (!ok[u]) continue;
-        const size_t row = p[u].row;
-        if (!isv) {
-            w[u] = __ldg(reinterpret_cast<const uint32_t*>(c.kc) + row * LPR + (l & 3) * BLK + (l >> 2));
-        } else {
-            const uint16_t* q = reinterpret_cast<const uint16_t*>(c.vc) + row * (D / 4) + (2 * (l & 3)) * BLK + (l >> 2);
-            w[u] = uint32_t(__ldg(q)) | uint32_t(__ldg(q + BLK)) << 16;
-        }
-        const ParAt at = par_at(row, gi, ng, isv);
-        const uint16_t* pp = isv ? c.vp : c.kp;
-        sz[u][0] = __ldg(pp + at.s);
-        sz[u][1] = __ldg(pp + at.z);
+        if (!isv) word[u] = __ldg(kc + row * LPR);
+        else word[u] = uint32_t(__ldg(vc + row * (D / 4))) | uint32_t(__ldg(vc + row * (D / 4) + BLK)) << 16;
+        const ParAt at = par_at(row, l / LPG, NG, isv);
+        sz[u] = uint32_t(__ldg(pp + at.s)) | uint32_t(__ldg(pp + at.z)) << 16;
     }
+    w = w0;
+    E* base = static_cast<E*>(isv ? v : k) + w.b * st.b + l * 8;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-        if (!ok[u]) continue;
-        const float s = __half2float(__ushort_as_half(sz[u][0])), z = __half2float(__ushort_as_half(sz[u][1]));
-        float f[8];
+        if (ok[u]) {
+            const float2 p = h2_to_f2(sz[u]);
+            float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float code = __uint_as_float(((w[u] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f;
-            f[i] = fmaf(code, s, z);
-            if (T == KV4_F16) f[i] = fminf(fmaxf(f[i], -65504.f), 65504.f);
+            for (int i = 0; i < 8; ++i)
+                f[i] = fmaf(__uint_as_float(((word[u] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f, p.x, p.y);
+            E* q = base + w.t * st.t + w.h * st.h;
+            if (T == KV4_F16) {
+                uint4 o;
+                __half2* h = reinterpret_cast<__half2*>(&o);
+                const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), bottom = __half2half2(__ushort_as_half(0xFBFF));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = __hmax2(__hmin2(__floats2half2_rn(f[2 * i], f[2 * i + 1]), top), bottom);
+                if (aligned16(q)) *reinterpret_cast<uint4*>(q) = o;
+                else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] = reinterpret_cast<const E*>(&o)[i];
+                }
+            } else {
+                store8<T>(q, aligned16(q), f);
+            }
         }
-        E* q = static_cast<E*>(isv ? v : k) + p[u].b * st.b + p[u].t * st.t + p[u].h * st.h + l * 8;
-        store8<T>(q, aligned16(q), f);
+        next_row(A, w);
     }
 }
 
@@ -1180,17 +1215,35 @@ cudaError_t launch_attention_t(const AttnArgs& A, const Plan& p, cudaStream_t st
 template <int D>
 RowArgs row_args(const Kv4& c, const Kv4Strides& ks, const Kv4Strides& vs, int n, const int32_t* start,
                  const int32_t* n_tok) {
-    return RowArgs{c, ks, vs, start, n_tok, n, int((int64_t(n) * c.heads + rows_per_block<D>() - 1) / rows_per_block<D>())};
+    constexpr int step = 256 / (D / 8);
+    return RowArgs{c, ks, vs, start, n_tok, n, int((int64_t(n) * c.heads + rows_per_block<D>() - 1) / rows_per_block<D>()),
+                   step / c.heads, step % c.heads};
 }
-template <int T, int D>
-cudaError_t append_t(const RowArgs& A, const void* k, const void* v, cudaStream_t st) {
-    kv4_append_kernel<T, D><<<dim3(unsigned(A.chunks) * A.c.batch, 2), 256, 0, st>>>(A, k, v);
+template <int D, int NG, int T>
+cudaError_t rows_t(const RowArgs& A, bool read, void* k, void* v, cudaStream_t st) {
+    const dim3 grid(unsigned(A.chunks) * A.c.batch, 2);
+    if (read) kv4_read_kernel<T, D, NG><<<grid, 256, 0, st>>>(A, k, v);
+    else kv4_append_kernel<T, D, NG><<<grid, 256, 0, st>>>(A, k, v);
     return cudaGetLastError();
 }
-template <int T, int D>
-cudaError_t read_t(const RowArgs& A, void* k, void* v, cudaStream_t st) {
-    kv4_read_kernel<T, D><<<dim3(unsigned(A.chunks) * A.c.batch, 2), 256, 0, st>>>(A, k, v);
-    return cudaGetLastError();
+template <int D, int NG>
+cudaError_t rows_ng(const RowArgs& A, int type, bool read, void* k, void* v, cudaStream_t st) {
+    if (type == KV4_F16) return rows_t<D, NG, KV4_F16>(A, read, k, v, st);
+    if (type == KV4_BF16) return rows_t<D, NG, KV4_BF16>(A, read, k, v, st);
+    return rows_t<D, NG, KV4_F32>(A, read, k, v, st);
+}
+cudaError_t rows(const Kv4& c, void* k, void* v, const Kv4Strides& ks, const Kv4Strides& vs, int type, bool read, int n,
+                 const int32_t* start, const int32_t* n_tok, cudaStream_t st) {
+    const int ng = c.dim / c.group;
+    if (c.dim == 128) {
+        const RowArgs A = row_args<128>(c, ks, vs, n, start, n_tok);
+        if (ng == 4) return rows_ng<128, 4>(A, type, read, k, v, st);
+        if (ng == 2) return rows_ng<128, 2>(A, type, read, k, v, st);
+        return rows_ng<128, 1>(A, type, read, k, v, st);
+    }
+    const RowArgs A = row_args<64>(c, ks, vs, n, start, n_tok);
+    if (ng == 2) return rows_ng<64, 2>(A, type, read, k, v, st);
+    return rows_ng<64, 1>(A, type, read, k, v, st);
 }
 
 }  // namespace
@@ -1198,27 +1251,13 @@ cudaError_t read_t(const RowArgs& A, void* k, void* v, cudaStream_t st) {
 extern "C" cudaError_t kie_launch_kv4_append(const Kv4* c, const void* k, const void* v, const Kv4Strides* ks,
                                              const Kv4Strides* vs, int type, int n, const int32_t* start,
                                              const int32_t* n_tok, cudaStream_t st) {
-    if (c->dim == 128) {
-        const RowArgs A = row_args<128>(*c, *ks, *vs, n, start, n_tok);
-        return type == KV4_F16 ? append_t<KV4_F16, 128>(A, k, v, st) : type == KV4_BF16 ? append_t<KV4_BF16, 128>(A, k, v, st)
-                                                                                       : append_t<KV4_F32, 128>(A, k, v, st);
-    }
-    const RowArgs A = row_args<64>(*c, *ks, *vs, n, start, n_tok);
-    return type == KV4_F16 ? append_t<KV4_F16, 64>(A, k, v, st) : type == KV4_BF16 ? append_t<KV4_BF16, 64>(A, k, v, st)
-                                                                                  : append_t<KV4_F32, 64>(A, k, v, st);
+    return rows(*c, const_cast<void*>(k), const_cast<void*>(v), *ks, *vs, type, false, n, start, n_tok, st);
 }
 
 extern "C" cudaError_t kie_launch_kv4_read(const Kv4* c, void* k, void* v, const Kv4Strides* ks, const Kv4Strides* vs,
                                            int type, int n, const int32_t* start, const int32_t* n_tok,
                                            cudaStream_t st) {
-    if (c->dim == 128) {
-        const RowArgs A = row_args<128>(*c, *ks, *vs, n, start, n_tok);
-        return type == KV4_F16 ? read_t<KV4_F16, 128>(A, k, v, st) : type == KV4_BF16 ? read_t<KV4_BF16, 128>(A, k, v, st)
-                                                                                     : read_t<KV4_F32, 128>(A, k, v, st);
-    }
-    const RowArgs A = row_args<64>(*c, *ks, *vs, n, start, n_tok);
-    return type == KV4_F16 ? read_t<KV4_F16, 64>(A, k, v, st) : type == KV4_BF16 ? read_t<KV4_BF16, 64>(A, k, v, st)
-                                                                                : read_t<KV4_F32, 64>(A, k, v, st);
+    return rows(*c, k, v, *ks, *vs, type, true, n, start, n_tok, st);
 }
 
 // Floats of workspace.  Stream form: a partial of CTA i for item k lies at slot k +
