@@ -295,24 +295,33 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     const float top_p = A.top_p ? A.top_p[row] : 1.f;
     const bool use_k = top_k > 0 && top_k < A.vocab, use_p = top_p < 1.f;
 
+    const float min_p = A.min_p ? A.min_p[row] : 0.f;
+    const uint64_t wmin = min_p > 0.f ? uint64_t(ceil(double(fminf(min_p, 1.f)) * double(1ull << FRAC))) : 0ull;
+    // warp `warp` holds elements [i0, i1) of the slice where order matters
+    const int per = (n + NWARP * 32 - 1) / (NWARP * 32) * 32;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+
     constexpr int ABOVE = -2, BELOW = -3;
     // Histogram of the elements for which binf gives a bin (>= 0), summed over the
     // cluster: afterwards each CTA holds its share of the sums in fc/fm[which] and,
     // where `sums` asks for it, the masses of what binf calls ABOVE and BELOW are in
     // above and below.
-    uint64_t above = 0, below = 0;
+    // `mine` is then this thread's part, over its warp's range of the slice, of what is
+    // above and not cut by min-p.
+    uint64_t above = 0, below = 0, mine = 0;
     auto histogram = [&](int which, auto binf, auto sums) {
         for (int i = tid; i < 4 * NB; i += NT) (&sh.h[0][0])[i] = 0u;
         __syncthreads();
         uint64_t sa = 0, sb = 0;
-        for (int i = tid; i < n; i += NT) {
+        for (int i = i0 + lane; i < i1; i += 32) {
             const float l = x[i];
             const int b = binf(l);
             if (b >= 0 || (sums.value && b != -1)) {
                 const uint64_t w = R.weight(l);
-                if (b < 0) {
+                if (sums.value && b < 0) {
                     sa += b == ABOVE ? w : 0ull;
                     sb += b == ABOVE ? 0ull : w;
+                    mine += b == ABOVE && w >= wmin ? w : 0ull;
                 } else {
                     atomicAdd(&sh.h[0][b], 1u);
                 }
@@ -481,8 +490,6 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         }
     };
 
-    const float min_p = A.min_p ? A.min_p[row] : 0.f;
-    const uint64_t wmin = min_p > 0.f ? uint64_t(ceil(double(fminf(min_p, 1.f)) * double(1ull << FRAC))) : 0ull;
     const float uf = A.u[row];
     const uint64_t U = uf >= 1.f ? ~0ull : uf > 0.f ? uint64_t(double(uf) * 18446744073709551616.0) : 0ull;
     // the least mass that is at least p of `mass`, and at least one token's
@@ -496,10 +503,6 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         if (A.tokens2) A.tokens2[row] = token;
         if (A.probs) A.probs[row] = float(double(w) / double(total));
     };
-    // warp `warp` holds elements [i0, i1) of the slice where order matters
-    const int per = (n + NWARP * 32 - 1) / (NWARP * 32) * 32;
-    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
-
     if (use_k && top_k <= KLIM) {
         // ---- sorted path: the bins that hold the first top_k tokens go to CTA 0
         for (int i = tid; i < NB; i += NT) sh.h[0][i] = 0u;
@@ -601,6 +604,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
 
     // ---- the kept prefix: every logit above `key`, and the n_eq lowest-indexed equal to it
     uint32_t key = 0u, n_eq = 0xFFFFFFFFu, all_eq = 0u;
+    float counted = -1.f;                // logits of a smaller 16 y are in `mine` already
     if (use_k) {
         histogram(0, [&](float l) { return bin_of(R.y(l)); }, std::false_type());
         select(false, uint64_t(top_k), 0ull);
@@ -651,6 +655,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         __syncthreads();
         const int b1 = sh.f_bin, b2 = int(sh.f_n);
         __syncthreads();
+        counted = float(b1);
         histogram(0, [&](float l) { const int b = bin_of(R.y(l)); return b < b1 ? ABOVE : b > b2 ? BELOW : b; }, std::true_type());
         const uint64_t head = above;
         uint64_t inside;
@@ -685,34 +690,37 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     }
     // past this y a weight is below min_p (half a percent more, for the rounding of both)
     const float ymax = min_p > 0.f ? -log2f(fminf(min_p, 1.f)) * 1.005f + 0.005f : INFINITY;
-    // kept mass of element i (lanes in index order); eq: equal tokens before this group of 32
-    auto kept = [&](int i, uint32_t& eq) -> uint64_t {
-        const float l = i < i1 ? x[i] : -INFINITY;
+    // kept mass of element i < end (lanes in index order); eq: equal tokens before this group of 32
+    auto kept = [&](int i, int end, uint32_t& eq, float from) -> uint64_t {
+        const float l = i < end ? x[i] : -INFINITY;
+        const float y = R.y(l);
         const uint32_t k = key_of<T>(l);
-        bool keep = i < i1 && k >= key && R.y(l) < ymax;
+        bool keep = i < end && k >= key && y < ymax && y * 16.f >= from;
         if (ties) {
-            const uint32_t same = __ballot_sync(0xffffffffu, i < i1 && k == key);
+            const uint32_t same = __ballot_sync(0xffffffffu, i < end && k == key);
             if (k == key) keep = keep && eq + __popc(same & ((1u << lane) - 1u)) < n_eq;
             eq += __popc(same);
         }
-        if (!keep) return 0;
-        const uint64_t w = R.weight(l);
+        if (!__any_sync(0xffffffffu, keep)) return 0;
+        const uint64_t w = keep ? R.weight(l) : 0;
         return w >= wmin ? w : 0;
     };
-    uint64_t sum = 0;
-    {
+    uint64_t sum = mine;
+    if (!use_k && !use_p && min_p <= 0.f) {
+        for (int i = i0 + lane; i < i1; i += 32) sum += R.weight(x[i]);
+    } else {
         uint32_t eq = eq0;
-        for (int i = i0; i < i1; i += 32) sum += kept(i + lane, eq);
+        for (int i = i0; i < i1; i += 32) sum += kept(i + lane, i1, eq, counted);
     }
     sum = warp_sum64(sum);
     __syncthreads();
     if (lane == 0) sh.wsum[warp] = sum;
+    if (ties && lane == 0) sh.wmin[warp] = eq0;
     __syncthreads();
-    if (tid == 0) {
-        uint64_t a = 0;
-        for (int w = 0; w < NWARP; ++w) a += sh.wsum[w];
-        sh.xch[ex][2] = a;
-    }
+    uint64_t cta = 0;
+#pragma unroll
+    for (int w = 0; w < NWARP; ++w) cta += sh.wsum[w];
+    if (tid == 0) sh.xch[ex][2] = cta;
     sync();
     uint64_t total = 0, start = 0;
     for (int r = 0; r < C; ++r) {
@@ -720,24 +728,44 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         if (r < rank) start += v;
         total += v;
     }
-    for (int w = 0; w < warp; ++w) start += sh.wsum[w];
     const uint64_t target = __umul64hi(total, U);
-    if (start <= target && target < start + sum) {       // this warp holds the crossing
-        uint32_t eq = eq0;
-        for (int i = i0; i < i1; i += 32) {
-            const uint64_t w = kept(i + lane, eq);
-            uint64_t inc = w;
+    if (start <= target && target < start + cta) {       // this CTA holds the crossing: all its warps look
+        int cw = 0;
+        while (start + sh.wsum[cw] <= target) start += sh.wsum[cw++];
+        const int c0 = min(n, cw * per), c1 = min(n, c0 + per);          // the crossing warp's range, cut into NWARP
+        const int part = (c1 - c0 + NWARP * 32 - 1) / (NWARP * 32) * 32, b0 = min(c1, c0 + warp * part), b1 = min(c1, b0 + part);
+        uint32_t eq = ties ? sh.wmin[cw] : 0u;
+        if (ties) {                                       // equal tokens before this warp's part
+            uint32_t e = 0;
+            for (int i = c0 + lane; i < b0; i += 32) e += key_of<T>(x[i]) == key;
+            eq += __reduce_add_sync(0xffffffffu, e);
+        }
+        uint64_t own = 0;
+        {
+            uint32_t e = eq;
+            for (int i = b0; i < b1; i += 32) own += kept(i + lane, b1, e, -1.f);
+        }
+        own = warp_sum64(own);
+        __syncthreads();                                  // the warps' sums have been read
+        if (lane == 0) sh.wsum[warp] = own;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) start += sh.wsum[w];
+        if (start <= target && target < start + own) {
+            for (int i = b0; i < b1; i += 32) {
+                const uint64_t w = kept(i + lane, b1, eq, -1.f);
+                uint64_t inc = w;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint64_t v = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += v;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+                    if (lane >= d) inc += v;
+                }
+                const uint32_t hit = __ballot_sync(0xffffffffu, start + inc > target);
+                if (hit) {
+                    if (lane == __ffs(hit) - 1) choose(s0 + i + lane, w, total);
+                    break;
+                }
+                start += __shfl_sync(0xffffffffu, inc, 31);
             }
-            const uint32_t hit = __ballot_sync(0xffffffffu, start + inc > target);
-            if (hit) {
-                if (lane == __ffs(hit) - 1) choose(s0 + i + lane, w, total);
-                break;
-            }
-            start += __shfl_sync(0xffffffffu, inc, 31);
         }
     }
     sync();                              // no CTA leaves while another may read its shared memory
