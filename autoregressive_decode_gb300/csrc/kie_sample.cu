@@ -39,6 +39,7 @@ namespace {
 
 constexpr int NT = 512, NWARP = NT / 32;   // threads per CTA
 constexpr int NB = 1024;                   // histogram bins (two per thread)
+constexpr int NF = 4 * NB;                 // bins of the approximate masses, a quarter as wide
 constexpr int FRAC = 44;                   // masses count 2^-44
 constexpr int LIST = 32;                   // candidates resolved by one warp
 constexpr int MAXC = 8;                    // CTAs per row
@@ -76,7 +77,7 @@ struct Shared {
     uint32_t f_cnt, f_n;
     uint64_t f_mass, f_m;
     // result of select()
-    uint32_t key, n_eq, all_eq;
+    uint32_t key, n_eq, all_eq, last;
     uint64_t mass;
     float chi, clo;
     int32_t token;
@@ -157,13 +158,13 @@ __device__ __forceinline__ int bin_of(float y) {
     return __float_as_int(__fadd_rd(fminf(y * 16.f, float(NB - 1)), 8388608.f)) - 0x4B000000;
 }
 
-template <int T>
-__global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const int S) {
+template <int T, int C>
+__global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const int S) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
     float* x = reinterpret_cast<float*>(smem_raw + (sizeof(Shared) + 15) / 16 * 16);
     cg::cluster_group cl = cg::this_cluster();
-    const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    const int rank = C > 1 ? int(cl.block_rank()) : 0;
     const int row = int(blockIdx.x) / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s0 = min(rank * S, A.vocab), n = min(S, A.vocab - s0);
     int ex = 0;   // exchange number: its values stay put for three more exchanges
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     }
     sync();
     mx = -INFINITY;
+#pragma unroll
     for (int r = 0; r < C; ++r) mx = fmaxf(mx, __uint_as_float(uint32_t(cl.map_shared_rank(&sh, r)->xch[ex][0])));
     ex = (ex + 1) & 3;
 
@@ -340,6 +342,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         sync();
         if (sums.value) {
             above = below = 0;
+#pragma unroll
             for (int r = 0; r < C; ++r) {
                 above += cl.map_shared_rank(&sh, r)->xch[ex][0];
                 below += cl.map_shared_rank(&sh, r)->xch[ex][1];
@@ -351,6 +354,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
             const int b = rank * per + i;
             uint32_t cnt = 0;
             uint64_t ms = 0;
+#pragma unroll
             for (int r = 0; r < C; ++r) {
                 const Shared* o = cl.map_shared_rank(&sh, r);
                 cnt += o->h[0][b];
@@ -458,6 +462,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
                 int32_t idx = 0x7FFFFFFF;
                 uint64_t w = 0;
                 int k = lane;
+#pragma unroll
                 for (int r = 0; r < C; ++r) {
                     const Shared* o = cl.map_shared_rank(&sh, r);
                     const int m = int(o->list_n);
@@ -503,72 +508,135 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         if (A.tokens2) A.tokens2[row] = token;
         if (A.probs) A.probs[row] = float(double(w) / double(total));
     };
+    // Where the running sum of val(bin, words summed over the cluster) over the bins of the
+    // single-word histogram `hist` reaches the targets aim(sum of all): the bins go to f_bin
+    // and f_n, the running sum with the first of them to f_mass.  Each CTA sums its share of
+    // the bins (every CTA reading all of 4,096 bins of 8 CTAs took 7 us).  The bin beyond the
+    // last stands for a target that is not reached.
+    auto crossing = [&](const uint32_t* hist, auto bins, auto val, auto aim) {
+        constexpr int N = decltype(bins)::value, PER = N / C, PT = PER > NT ? PER / NT : 1;
+        const int at = tid * PT, bin = rank * PER + at;
+        if (tid == 0) { sh.f_bin = N; sh.f_n = N; sh.f_mass = ~0ull; }
+        sync();
+        uint64_t q[PT], qs = 0, all;
+#pragma unroll
+        for (int j = 0; j < PT; ++j) q[j] = 0;
+        if (at < PER) {
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                const uint32_t* o = cl.map_shared_rank(const_cast<uint32_t*>(hist), r) + bin;
+#pragma unroll
+                for (int j = 0; j < PT; ++j) q[j] += o[j];
+            }
+#pragma unroll
+            for (int j = 0; j < PT; ++j) {
+                q[j] = val(bin + j, q[j]);
+                qs += q[j];
+            }
+        }
+        uint64_t before = block_prefix(qs, all);
+        if (tid == 0) sh.xch[ex][0] = all;
+        sync();
+        all = 0;
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            const uint64_t v = cl.map_shared_rank(&sh, r)->xch[ex][0];
+            before += r < rank ? v : 0ull;
+            all += v;
+        }
+        ex = (ex + 1) & 3;
+        const ulonglong2 t = aim(all);
+        if (at < PER) {
+#pragma unroll
+            for (int j = 0; j < PT; ++j) {
+                const uint64_t with = before + q[j];
+                if (before < t.x && t.x <= with)
+                    for (int r = 0; r < C; ++r) { Shared* o = cl.map_shared_rank(&sh, r); o->f_bin = bin + j; o->f_mass = with; }
+                if (before < t.y && t.y <= with)
+                    for (int r = 0; r < C; ++r) cl.map_shared_rank(&sh, r)->f_n = uint32_t(bin + j);
+                before = with;
+            }
+        }
+        sync();
+    };
+    // Bitonic sort of fm[1][0 .. np) (np a power of two from 64 to CAP), ascending.
+    auto sort = [&](int np) {
+        for (int k = 2; k <= np; k *= 2)
+            for (int j = k / 2; j > 0; j /= 2) {
+                if (tid < np / 2) {
+                    const int i = ((tid & ~(j - 1)) << 1) | (tid & (j - 1));
+                    const uint64_t lo = sh.fm[1][i], hi = sh.fm[1][i | j];
+                    if ((lo > hi) == ((i & k) == 0)) { sh.fm[1][i] = hi; sh.fm[1][i | j] = lo; }
+                }
+                // a warp's 32 pairs of a step j <= 32 are its own 64 elements; the next step's too
+                // unless it is a longer one
+                if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
+                else __syncwarp();
+            }
+        __syncthreads();
+    };
+
+    uint64_t* list = reinterpret_cast<uint64_t*>(sh.h[2]);   // CAP candidates, once the histogram has been summed
     if (use_k && top_k <= KLIM) {
         // ---- sorted path: the bins that hold the first top_k tokens go to CTA 0
-        for (int i = tid; i < NB; i += NT) sh.h[0][i] = 0u;
+        uint32_t* hist = sh.h[0];
+        for (int i = tid; i < NB; i += NT) hist[i] = 0u;
         __syncthreads();
-        for (int i = tid; i < n; i += NT) atomicAdd(&sh.h[0][bin_of(R.y(x[i]))], 1u);
-        sync();
-        uint32_t c[2] = {0u, 0u}, earlier[2] = {0u, 0u};
-        for (int r = 0; r < C; ++r) {
-            const uint2 v = *reinterpret_cast<const uint2*>(&cl.map_shared_rank(&sh, r)->h[0][2 * tid]);
-            c[0] += v.x;
-            c[1] += v.y;
-            if (r < rank) { earlier[0] += v.x; earlier[1] += v.y; }
-        }
-        uint64_t all;
-        uint32_t before = uint32_t(block_prefix(c[0] + c[1], all));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (before < uint32_t(top_k) && uint32_t(top_k) <= before + c[j]) { sh.f_bin = 2 * tid + j; sh.f_n = before + c[j]; }
-            before += c[j];
-        }
-        __syncthreads();
-        const int b = sh.f_bin, nc = int(sh.f_n);
+        for (int i = tid; i < n; i += NT) atomicAdd(&hist[bin_of(R.y(x[i]))], 1u);
+        crossing(hist, std::integral_constant<int, NB>(), [](int, uint64_t v) { return v; },
+                 [&](uint64_t) { return ulonglong2{uint64_t(top_k), uint64_t(top_k)}; });
+        const int b = sh.f_bin, nc = sh.f_mass <= CAP ? int(sh.f_mass) : CAP + 1;
         if (nc <= CAP) {
-            uint32_t base = uint32_t(block_sum((2 * tid <= b ? earlier[0] : 0u) + (2 * tid + 1 <= b ? earlier[1] : 0u)));
-            // the candidates in index order
-            uint32_t mine = 0;
-            const float yend = b < NB - 1 ? float(b + 1) : INFINITY;   // bin <= b: 16 y below b + 1
-            auto in_bins = [&](float l) { return b == NB - 1 || R.y(l) * 16.f < yend; };
-            for (int i = i0 + lane; i < i1; i += 32) mine += in_bins(x[i]);
-            mine = __reduce_add_sync(0xffffffffu, mine);
-            if (lane == 0) sh.wcnt[warp] = mine;
+            // this CTA's candidates in index order; bin <= b: 16 y below b + 1
+            const float yend = b < NB - 1 ? float(b + 1) : INFINITY;
+            auto in_bins = [&](float l) { return R.y(l) * 16.f < yend || b == NB - 1; };
+            uint32_t cw = 0, base = 0, own = 0;
+            for (int i = i0 + lane; i < i1; i += 32) cw += in_bins(x[i]);
+            cw = __reduce_add_sync(0xffffffffu, cw);
+            if (lane == 0) sh.wcnt[warp] = cw;
             __syncthreads();
-            for (int w = 0; w < warp; ++w) base += sh.wcnt[w];
-            Shared* o = cl.map_shared_rank(&sh, 0);
-            for (int i = i0; i < i1; i += 32) {
+#pragma unroll
+            for (int w = 0; w < NWARP; ++w) {
+                base += w < warp ? sh.wcnt[w] : 0u;
+                own += sh.wcnt[w];
+            }
+            for (int i = i0; cw && i < i1; i += 32) {
                 const float l = i + lane < i1 ? x[i + lane] : 0.f;
                 const bool in = i + lane < i1 && in_bins(l);
                 const uint32_t hit = __ballot_sync(0xffffffffu, in);
-                if (in) {
-                    const uint32_t at = base + __popc(hit & ((1u << lane) - 1u));
-                    o->h[1][at] = key_of<T>(l);
-                    o->h[2][at] = uint32_t(s0 + i + lane);
-                    o->fm[0][at] = R.weight(l);
-                }
+                if (in) list[base + __popc(hit & ((1u << lane) - 1u))] = uint64_t(key_of<T>(l)) << 32 | uint32_t(s0 + i + lane);
                 base += __popc(hit);
             }
+            if (tid == 0) sh.xch[ex][0] = own;
             sync();
-            if (rank != 0) return;       // CTA 0 reads its own shared memory alone from here on
+            if (rank != 0) {
+                cl.barrier_arrive();
+                cl.barrier_wait();       // CTA 0 has read the list
+                return;
+            }
+            int cnt[C];
+#pragma unroll
+            for (int r = 0; r < C; ++r) cnt[r] = int(cl.map_shared_rank(&sh, r)->xch[ex][0]);
             int np = 64;
             while (np < nc) np *= 2;
-            for (int i = tid; i < np; i += NT) sh.fm[1][i] = i < nc ? uint64_t(~sh.h[1][i]) << 32 | uint32_t(i) : ~0ull;
-            __syncthreads();
-            // bitonic sort, ascending: logit descending, index ascending
-            for (int k = 2; k <= np; k *= 2)
-                for (int j = k / 2; j > 0; j /= 2) {
-                    if (tid < np / 2) {
-                        const int i = ((tid & ~(j - 1)) << 1) | (tid & (j - 1));
-                        const uint64_t lo = sh.fm[1][i], hi = sh.fm[1][i | j];
-                        if ((lo > hi) == ((i & k) == 0)) { sh.fm[1][i] = hi; sh.fm[1][i | j] = lo; }
-                    }
-                    // a warp's 32 pairs of a step j <= 32 are its own 64 elements; the next step's too
-                    // unless it is a longer one
-                    if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
-                    else __syncwarp();
+            for (int i = tid; i < np; i += NT) {
+                uint64_t v = 0;
+                int at = i;
+#pragma unroll
+                for (int r = 0; r < C; ++r) {
+                    if (at >= 0 && at < cnt[r]) v = cl.map_shared_rank(list, r)[at];
+                    at = at < cnt[r] ? -1 : at - cnt[r];
                 }
+                if (i < nc) {
+                    const uint32_t k = uint32_t(v >> 32);
+                    sh.fc[1][i] = uint32_t(v);
+                    sh.fm[0][i] = R.weight(of_key<T>(k));
+                    sh.fm[1][i] = uint64_t(~k) << 32 | uint32_t(i);
+                } else sh.fm[1][i] = ~0ull;
+            }
+            if (C > 1) cl.barrier_arrive();
             __syncthreads();
+            sort(np);
             int pos[2];
             uint64_t w[2], total;
 #pragma unroll
@@ -594,17 +662,19 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
             const uint64_t draw = __umul64hi(total, U);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (mb <= draw && draw < mb + w[j]) choose(int(sh.h[2][2 * tid + j]), w[j], total);
+                if (mb <= draw && draw < mb + w[j]) choose(int(sh.fc[1][2 * tid + j]), w[j], total);
                 mb += w[j];
             }
+            if (C > 1) cl.barrier_wait();
             return;
         }
-        __syncthreads();
     }
 
-    // ---- the kept prefix: every logit above `key`, and the n_eq lowest-indexed equal to it
-    uint32_t key = 0u, n_eq = 0xFFFFFFFFu, all_eq = 0u;
+    // ---- the kept prefix: every logit above `key`, and of those equal to it the n_eq lowest-
+    // indexed, or all up to index `last`
+    uint32_t key = 0u, n_eq = 0xFFFFFFFFu, all_eq = 0u, last = 0xFFFFFFFFu;
     float counted = -1.f;                // logits of a smaller 16 y are in `mine` already
+    bool summed = false;                 // or all are
     if (use_k) {
         histogram(0, [&](float l) { return bin_of(R.y(l)); }, std::false_type());
         select(false, uint64_t(top_k), 0ull);
@@ -617,55 +687,123 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
             key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
         }
     } else if (use_p) {
-        // masses of the bins to 2^-14: 2^(f / 16) in units of 2^-14, f the distance to the bin's end
-        for (int i = tid; i < NB; i += NT) sh.h[0][i] = 0u;
+        // masses of the fine bins to 2^-14: 2^(f / 64) in units of 2^-14, f the distance to the bin's end
+        uint32_t* hist = &sh.h[0][0];
+        for (int i = tid; i < NF; i += NT) hist[i] = 0u;
+        if (tid == 0) sh.list_n = 0u;
         __syncthreads();
         for (int i = tid; i < n; i += NT) {
-            const float y = R.y(x[i]) * 16.f;
-            if (y < 46.f * 16.f) {
+            const float y = R.y(x[i]) * 64.f;
+            if (y < 46.f * 64.f) {
                 const float down = __fadd_rd(y, 8388608.f);
-                float v;                   // in [1, 2^(1/16)]: its first 14 fraction bits
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(fmaf(down - 8388608.f - y, 1.f / 16.f, 1.f / 16.f)));
-                atomicAdd(&sh.h[0][__float_as_int(down) - 0x4B000000], (__float_as_uint(v) - 0x3F000000u) >> 9);
+                float v;                   // in [1, 2^(1/64)]: rounded to 14 fraction bits
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(fmaf(down - 8388608.f - y, 1.f / 64.f, 1.f / 64.f)));
+                atomicAdd(&hist[__float_as_int(down) - 0x4B000000], (__float_as_uint(v) - 0x3F000000u + 256u) >> 9);
             }
         }
+        // The prefix ends where the mass passes p of the total, both sums of words good to 2^-15 and
+        // to y's rounding, 2^-18 of a weight, in units of 2^-40 (2^18 tokens at most): within a
+        // 2^-13th of the target.
+        crossing(hist, std::integral_constant<int, NF>(),
+                 [](int bin, uint64_t v) { return uint64_t(float(v) * exp2f(26.f - float(bin + 1) / 64.f)); },
+                 [&](uint64_t total) {
+                     const float want = fmaxf(top_p, 0.f) * float(total);
+                     return ulonglong2{uint64_t(fmaxf(want * (1.f - 1.f / 8192.f), 1.f)), uint64_t(fmaxf(want * (1.f + 1.f / 8192.f), 1.f))};
+                 });
+        const int b1 = min(sh.f_bin, NF - 1), b2 = min(int(sh.f_n), NF - 1);
+        const float y1 = float(b1), y2 = b2 < NF - 1 ? float(b2 + 1) : INFINITY;    // the bins [b1, b2]: 64 y in [y1, y2)
+        // the one exact pass: sums before and after those bins, their tokens to a list
+        uint64_t sa = 0, sb = 0;
+        for (int i = i0 + lane; i < i1; i += 32) {
+            const float l = x[i], y = R.y(l) * 64.f;
+            if (y >= y1 && y < y2) {
+                const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                if (at < CAP) list[at] = uint64_t(~key_of<T>(l)) << 32 | uint32_t(s0 + i);
+            } else {
+                const uint64_t w = R.weight(l);
+                sa += y < y1 ? w : 0ull;
+                sb += y < y1 ? 0ull : w;
+                mine += y < y1 && w >= wmin ? w : 0ull;
+            }
+        }
+        sa = block_sum(sa);
+        sb = block_sum(sb);
+        if (tid == 0) { sh.xch[ex][0] = sa; sh.xch[ex][1] = sb; sh.xch[ex][2] = sh.list_n; }
         sync();
-        float q[2] = {0.f, 0.f};
+        uint64_t head = 0, tail = 0;
+        int cnt[C], nc = 0, cnt_own = 0;
+#pragma unroll
         for (int r = 0; r < C; ++r) {
-            const uint2 v = *reinterpret_cast<const uint2*>(&cl.map_shared_rank(&sh, r)->h[0][2 * tid]);
-            q[0] += float(v.x);
-            q[1] += float(v.y);
+            const uint64_t* v = cl.map_shared_rank(&sh, r)->xch[ex];
+            head += v[0];
+            tail += v[1];
+            cnt[r] = int(v[2]);
+            nc += cnt[r];
+            cnt_own = r == rank ? cnt[r] : cnt_own;
         }
-        // in units of 2^-40 (at most 2^18 tokens of 2^40): exact sums of what is good to 2^-13
-        uint64_t qi[2], total;
+        ex = (ex + 1) & 3;
+        if (nc <= CAP) {
+            if (rank == 0) {
+                int np = 64;
+                while (np < nc) np *= 2;
+                for (int i = tid; i < np; i += NT) {
+                    uint64_t v = ~0ull;
+                    int at = i;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) qi[j] = uint64_t(q[j] * exp2f(26.f - float(2 * tid + j + 1) / 16.f));
-        uint64_t before = block_prefix(qi[0] + qi[1], total);
-        // the prefix ends where the mass passes p of the total: both are within 2^-12
-        const float want = fmaxf(top_p, 0.f) * float(total), t1 = want * (1.f - 1.f / 2048.f), t2 = want * (1.f + 1.f / 2048.f);
-        if (tid == 0) { sh.f_bin = 0; sh.f_n = NB - 1; }
-        __syncthreads();
+                    for (int r = 0; r < C; ++r) {
+                        if (at >= 0 && at < cnt[r]) v = cl.map_shared_rank(list, r)[at];
+                        at = at < cnt[r] ? -1 : at - cnt[r];
+                    }
+                    sh.fm[1][i] = v;
+                }
+                __syncthreads();
+                sort(np);              // logit descending, index ascending
+                uint64_t w[2], inside;
+                uint32_t k2[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float lo = float(before), hi = float(before + qi[j]);
-            if (lo < t1 && t1 <= hi) sh.f_bin = 2 * tid + j;
-            if (lo < t2 && t2 <= hi) sh.f_n = uint32_t(2 * tid + j);
-            before += qi[j];
-        }
-        __syncthreads();
-        const int b1 = sh.f_bin, b2 = int(sh.f_n);
-        __syncthreads();
-        counted = float(b1);
-        histogram(0, [&](float l) { const int b = bin_of(R.y(l)); return b < b1 ? ABOVE : b > b2 ? BELOW : b; }, std::true_type());
-        const uint64_t head = above;
-        uint64_t inside;
-        {
+                for (int j = 0; j < 2; ++j) {
+                    const int i = 2 * tid + j;
+                    k2[j] = i < nc ? ~uint32_t(sh.fm[1][i] >> 32) : 0u;
+                    w[j] = i < nc ? R.weight(of_key<T>(k2[j])) : 0ull;
+                }
+                uint64_t mb = head + block_prefix(w[0] + w[1], inside);
+                const uint64_t target = p_target(head + inside + tail);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (mb < target && target <= mb + w[j]) { sh.key = k2[j]; sh.last = uint32_t(sh.fm[1][2 * tid + j]); }
+                    mb += w[j];
+                }
+            }
+            sync();
+            const Shared* o = cl.map_shared_rank(&sh, 0);
+            key = o->key;
+            last = o->last;
+            // the kept tokens of this CTA's list, to the sums of their warps' ranges
+            if (tid < NWARP) sh.wsum[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < cnt_own; i += NT) {
+                const uint64_t v = list[i];
+                if (v <= (uint64_t(~key) << 32 | last)) {
+                    const uint64_t w = R.weight(of_key<T>(~uint32_t(v >> 32)));
+                    if (w >= wmin) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.wsum[(int(uint32_t(v)) - s0) / per]), w);
+                }
+            }
+            __syncthreads();
+            mine += lane == 0 ? sh.wsum[warp] : 0ull;
+            summed = true;
+        } else {
+            // a crowd: histograms of exact masses
+            mine = 0;
+            const int c1 = b1 / 4, c2 = b2 / 4;
+            counted = float(c1);
+            histogram(0, [&](float l) { const int b = bin_of(R.y(l)); return b < c1 ? ABOVE : b > c2 ? BELOW : b; }, std::true_type());
+            const uint64_t first = above;
             const Shared* o = cl.map_shared_rank(&sh, (2 * tid) / (NB / C));
-            inside = block_sum(o->fm[0][2 * tid] + o->fm[0][2 * tid + 1]);
+            const uint64_t inside = block_sum(o->fm[0][2 * tid] + o->fm[0][2 * tid + 1]);
+            select(true, p_target(first + inside + below), first);
+            __syncthreads();
+            key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
         }
-        select(true, p_target(above + inside + below), head);
-        __syncthreads();
-        key = sh.key; n_eq = sh.n_eq; all_eq = sh.all_eq;
     }
 
     // ---- masses in index order
@@ -695,7 +833,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
         const float l = i < end ? x[i] : -INFINITY;
         const float y = R.y(l);
         const uint32_t k = key_of<T>(l);
-        bool keep = i < end && k >= key && y < ymax && y * 16.f >= from;
+        bool keep = i < end && (k > key || (k == key && uint32_t(s0 + i) <= last)) && y < ymax && y * 16.f >= from;
         if (ties) {
             const uint32_t same = __ballot_sync(0xffffffffu, i < end && k == key);
             if (k == key) keep = keep && eq + __popc(same & ((1u << lane) - 1u)) < n_eq;
@@ -708,7 +846,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     uint64_t sum = mine;
     if (!use_k && !use_p && min_p <= 0.f) {
         for (int i = i0 + lane; i < i1; i += 32) sum += R.weight(x[i]);
-    } else {
+    } else if (!summed) {
         uint32_t eq = eq0;
         for (int i = i0; i < i1; i += 32) sum += kept(i + lane, i1, eq, counted);
     }
@@ -723,11 +861,14 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
     if (tid == 0) sh.xch[ex][2] = cta;
     sync();
     uint64_t total = 0, start = 0;
+#pragma unroll
     for (int r = 0; r < C; ++r) {
         const uint64_t v = cl.map_shared_rank(&sh, r)->xch[ex][2];
         if (r < rank) start += v;
         total += v;
     }
+    // no CTA leaves while another may read its shared memory: all of that is done here
+    if (C > 1) cl.barrier_arrive();
     const uint64_t target = __umul64hi(total, U);
     if (start <= target && target < start + cta) {       // this CTA holds the crossing: all its warps look
         int cw = 0;
@@ -768,11 +909,11 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleArgs A, const in
             }
         }
     }
-    sync();                              // no CTA leaves while another may read its shared memory
+    if (C > 1) cl.barrier_wait();
 }
 
-template <int T>
-cudaError_t launch(const SampleArgs& a, int C, int S, cudaStream_t st) {
+template <int T, int C>
+cudaError_t launch(const SampleArgs& a, int S, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const int smem = int((sizeof(Shared) + 15) / 16 * 16) + S * 4;
     int dev = 0;
@@ -780,7 +921,7 @@ cudaError_t launch(const SampleArgs& a, int C, int S, cudaStream_t st) {
     if (r != cudaSuccess) return r;
     const uint64_t bit = 1ull << (dev & 63);
     if (dev >= 64 || !(done.load(std::memory_order_acquire) & bit)) {
-        r = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        r = cudaFuncSetAttribute(sample_kernel<T, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         if (r != cudaSuccess) return r;
         if (dev < 64) done.fetch_or(bit, std::memory_order_release);
     }
@@ -796,7 +937,15 @@ cudaError_t launch(const SampleArgs& a, int C, int S, cudaStream_t st) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, S);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<T, C>, a, S);
+}
+
+template <int T>
+cudaError_t launch_t(const SampleArgs& a, int C, int S, cudaStream_t st) {
+    if (C == 1) return launch<T, 1>(a, S, st);
+    if (C == 2) return launch<T, 2>(a, S, st);
+    if (C == 4) return launch<T, 4>(a, S, st);
+    return launch<T, 8>(a, S, st);
 }
 
 }  // namespace
@@ -807,7 +956,7 @@ extern "C" cudaError_t kie_launch_sample(const SampleArgs* a, int sms, cudaStrea
     int C = 1;
     while (C < MAXC && (int64_t(a->rows) * C < 2 * sms || int64_t(a->vocab) > int64_t(C) * 32768) && a->vocab > C * 1024) C *= 2;
     const int S = ((a->vocab + C - 1) / C + 7) / 8 * 8;
-    if (a->type == 0) return launch<0>(*a, C, S, st);
-    if (a->type == 1) return launch<1>(*a, C, S, st);
-    return launch<2>(*a, C, S, st);
+    if (a->type == 0) return launch_t<0>(*a, C, S, st);
+    if (a->type == 1) return launch_t<1>(*a, C, S, st);
+    return launch_t<2>(*a, C, S, st);
 }
