@@ -1965,4 +1965,51 @@ kie_status kie_sample(const kie_sample_args* a, void* stream) {
     return KIE_OK;
 }
 
+kie_status kie_generate_sampled_device(kie_engine* e, const int32_t* first_tokens, int32_t n,
+                                       const kie_sampling* s, int32_t* d_out_tokens, float* d_out_probs) {
+    if (!e) return fail(nullptr, KIE_ERR_INVALID_ARG, "engine is NULL");
+    kie_status st = e->batched() ? ready_batch(e, n) : ready(e, n);
+    if (st != KIE_OK) return st;
+    if (e->cfg.vocab > KIE_SAMPLE_MAX_VOCAB) return fail(e, KIE_ERR_UNSUPPORTED, "vocabulary above %d", KIE_SAMPLE_MAX_VOCAB);
+    if (n == 0) return KIE_OK;
+    auto word = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (!first_tokens || !s || !s->u || !d_out_tokens || !word(s->u) || !word(d_out_tokens) || !word(d_out_probs) ||
+        !word(s->temperature) || !word(s->top_k) || !word(s->top_p) || !word(s->min_p))
+        return fail(e, KIE_ERR_INVALID_ARG, "NULL or misaligned pointer");
+    const int nb = e->batched() ? e->plan.nb : 1;
+    if ((st = check_tokens(e, first_tokens, nb)) != KIE_OK) return st;
+    DeviceScope dev(e->cfg.device);
+    if (!dev.ok) return fail(e, KIE_ERR_CUDA, "cudaSetDevice(%d) failed", e->cfg.device);
+    const int sms = sm_count(e->cfg.device);
+    if (sms < 1) return fail(e, KIE_ERR_CUDA, "no multiprocessor count");
+    // each step leaves its logits in the engine's workspace and the sampler its
+    // tokens where the next step reads its input
+    const bool graphs = e->cfg.mode != KIE_MODE_PERSISTENT;
+    float* d_log = reinterpret_cast<float*>(e->dev(nb > 1 ? e->lay.out_logits : e->lay.step_logits));
+    int32_t* d_in = e->batched() ? reinterpret_cast<int32_t*>(e->dev(e->lay.req))
+                                 : reinterpret_cast<int32_t*>(e->dev(e->lay.ctl) + offsetof(KieControl, tok));
+    SampleArgs a{d_log, KIE_FP32, nb, e->cfg.vocab, e->cfg.vocab, s->temperature, s->top_k, s->top_p, s->min_p,
+                 s->u, d_out_tokens, d_out_probs, d_in};
+    if (graphs) {
+        for (int f = 0; f < 2; ++f)
+            if ((st = ensure_graph(e, f)) != KIE_OK) return st;
+        if ((st = set_ctl(e, first_tokens[0], e->pos, false)) != KIE_OK) return st;
+    }
+    for (int t = 0; t < n; ++t) {
+        if (graphs) {
+            KIE_CUDA(e, cudaGraphLaunch(e->graph[tag_fill(e->cfg, e->pos)], e->stream));
+            e->pos += 1;
+        } else if (e->batched()) {
+            if ((st = run_batch(e, t == 0 ? first_tokens : nullptr, 1, nullptr, d_log)) != KIE_OK) return st;
+        } else {
+            if ((st = run_steps(e, 1, t == 0 ? first_tokens[0] : -1, nullptr, 0, nullptr, d_log)) != KIE_OK) return st;
+        }
+        KIE_CUDA(e, kie_launch_sample(&a, sms, e->stream));
+        a.u += nb;
+        a.tokens += nb;
+        if (a.probs) a.probs += nb;
+    }
+    return KIE_OK;
+}
+
 }  // extern "C"

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
     if (mx == -INFINITY) {               // nothing to choose from
         if (rank == 0 && tid == 0) {
             A.tokens[row] = -1;
-            if (A.tokens2) A.tokens2[row] = -1;
+            if (A.next) A.next[row] = 0;
             if (A.probs) A.probs[row] = 0.f;
         }
         sync();
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
         if (rank == 0 && tid == 0) {
             for (int r = 1; r < C; ++r) at = min(at, uint32_t(cl.map_shared_rank(&sh, r)->xch[ex][0]));
             A.tokens[row] = int32_t(at);
-            if (A.tokens2) A.tokens2[row] = int32_t(at);
+            if (A.next) A.next[row] = int32_t(at);
             if (A.probs) A.probs[row] = 1.f;
         }
         sync();
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
     };
     auto choose = [&](int token, uint64_t w, uint64_t total) {
         A.tokens[row] = token;
-        if (A.tokens2) A.tokens2[row] = token;
+        if (A.next) A.next[row] = token;
         if (A.probs) A.probs[row] = float(double(w) / double(total));
     };
     // Where the running sum of val(bin, words summed over the cluster) over the bins of the

@@ -15,7 +15,7 @@ struct SampleArgs {
     const float* u;              // [rows]
     int32_t* tokens;             // [rows]
     float* probs;                // [rows] or null
-    int32_t* tokens2;            // [rows] or null: a second copy of the tokens
+    int32_t* next;               // [rows] or null: the tokens again, 0 for -1 (an engine's next input)
 };
 
 // Largest vocabulary: row sums of 44-bit weights stay below 2^62.

@@ -74,6 +74,11 @@ class kie_sample_args(C.Structure):
                 ("device", C.c_int32)]
 
 
+class kie_sampling(C.Structure):
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p),
+                ("u", C.c_void_p)]
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "kie_workspace_bytes": (C.c_size_t, [C.POINTER(kie_config)]),
@@ -90,6 +95,8 @@ EXPORTS = {
     "kie_decode_batch": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "kie_generate_greedy_batch": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
     "kie_generate_greedy_batch_device": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
+    "kie_generate_sampled_device": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.POINTER(kie_sampling), C.c_void_p,
+                                              C.c_void_p]),
     "kie_reset": (C.c_int, [C.c_void_p]),
     "kie_get_pos": (C.c_int32, [C.c_void_p]),
     "kie_set_pos": (C.c_int, [C.c_void_p, C.c_int32]),
@@ -275,6 +282,31 @@ class Engine:
         f = np.ascontiguousarray(first_tokens, dtype=np.int32)
         _check(load().kie_generate_greedy_batch_device(self.h, _ptr(f), int(n), _ptr(d_tokens), _ptr(d_logits)),
                self.h)
+
+    # -- sampling ---------------------------------------------------------------------------
+    def generate_sampled_device(self, first_tokens, u, d_tokens, d_probs=None, temperature=None, top_k=None,
+                                top_p=None, min_p=None):
+        """kie_generate_sampled_device: len(u) steps of every request, tokens drawn
+        with the random numbers u (CUDA fp32 [n, batch]) into d_tokens (CUDA int32
+        [n, batch]) and their probabilities into d_probs (fp32); the parameters are
+        CUDA tensors [batch].  Enqueued on the engine's stream without
+        synchronising: that stream must see the tensors written, and they must
+        live until it is done."""
+        torch = _need_torch()
+        f = np.ascontiguousarray(first_tokens, dtype=np.int32).reshape(-1)
+        if f.size != self.batch:
+            raise ValueError(f"first_tokens must hold {self.batch} tokens")
+        n, b, dev, i32, f32 = len(u), self.batch, self.cfg.device, torch.int32, torch.float32
+        for t, dtype, what in ((u, f32, "u"), (d_tokens, i32, "d_tokens"), (d_probs, f32, "d_probs")):
+            if t is None and what == "d_probs":
+                continue
+            _on(t, dev, what)
+            if t.dtype is not dtype or t.shape != (n, b) or not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape ({n}, {b})")
+        s = kie_sampling(_vector(temperature, b, f32, dev, "temperature"), _vector(top_k, b, i32, dev, "top_k"),
+                         _vector(top_p, b, f32, dev, "top_p"), _vector(min_p, b, f32, dev, "min_p"), u.data_ptr())
+        _check(load().kie_generate_sampled_device(self.h, _ptr(f), n, C.byref(s), d_tokens.data_ptr(),
+                                                  _ptr(d_probs)), self.h)
 
     def sync(self):
         _check(load().kie_sync(self.h), self.h)

@@ -221,6 +221,26 @@ kie_status kie_generate_greedy_batch(kie_engine* e, const int32_t* first_tokens,
 kie_status kie_generate_greedy_batch_device(kie_engine* e, const int32_t* first_tokens, int32_t n,
                                             int32_t* d_out_tokens, float* d_out_logits);
 
+/* n steps of every request (one without batching) whose tokens are drawn from
+ * the logits as kie_sample does (below), equal to n rounds of a step and of
+ * kie_sample on its logits: token t + 1 of request b is drawn with u[t][b] from
+ * the logits after its token t and consumed by the step after that.  The
+ * parameters are DEVICE arrays, read by every step.  first_tokens: host
+ * [batch], read before the call returns.  d_out_tokens: device int32 [n][batch];
+ * d_out_probs: NULL or device fp32 [n][batch].  Logits that leave nothing give
+ * token -1, and the next step consumes token 0.  Enqueued on the engine's stream
+ * without synchronising, on every kind of engine with a vocabulary of at most
+ * 2^18 (else KIE_ERR_UNSUPPORTED).  Positions += n. */
+typedef struct {
+    const float* temperature;  /* [batch] or NULL: 1   */
+    const int32_t* top_k;      /* [batch] or NULL: off */
+    const float* top_p;        /* [batch] or NULL: off */
+    const float* min_p;        /* [batch] or NULL: off */
+    const float* u;            /* [n][batch] in [0, 1) */
+} kie_sampling;
+kie_status kie_generate_sampled_device(kie_engine* e, const int32_t* first_tokens, int32_t n,
+                                       const kie_sampling* sampling, int32_t* d_out_tokens, float* d_out_probs);
+
 /* Synchronise the engine's stream and report any error the GPU program set. */
 kie_status kie_sync(kie_engine* e);
 
@@ -465,8 +485,9 @@ kie_status kie_kv4_attention(const kie_kv4_cache* c, const kie_kv4_query* q, voi
  *   the token is the first, by id, at which the running mass of the kept ones
  *     exceeds u times their total (u is taken as 0 below 0, and as the largest
  *     number below 1 from 1 on); its probability is w / that total.
- * (a difference m - l_i beyond fp32's range counts as infinite).  Masses are exact sums of weights in units of 2^-44, so results do not depend
- * on how the work is split.  A logit of -infinity or NaN is never chosen;
+ * (a difference m - l_i beyond fp32's range counts as infinite).  Masses are
+ * exact sums of weights in units of 2^-44, so results do not depend on how the
+ * work is split.  A logit of -infinity or NaN is never chosen;
  * logits of +infinity share the mass; a row that leaves nothing gives token -1
  * and probability 0.  vocab is at most 2^18. */
 typedef struct {

@@ -105,3 +105,10 @@ def test_python_checks():
         kie._written(x[:1].expand(2, 8), "out")
     with pytest.raises(ValueError):
         kie._vector(x, 2, torch.int32, 0, "start")
+
+
+def test_sampled_generation_refuses_on_the_host():
+    lib = kie.load()
+    s = kie.kie_sampling(None, None, None, None, P)
+    assert lib.kie_generate_sampled_device(None, P, 1, C.byref(s), P, None) == BAD
+    assert lib.kie_last_error(None)
