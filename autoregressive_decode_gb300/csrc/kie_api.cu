@@ -1865,7 +1865,7 @@ Kv4Attn kv4_attn(const kie_kv4_cache* c, const kie_kv4_query* q) {
     a.kv_len = q->kv_len;
     a.n_tok = q->n_tok;
     a.causal = q->causal;
-    a.window = q->window;
+    a.window = std::min(q->window, c->max_ctx);   // no more keys than that; differences of positions stay in 32 bits
     a.scale = q->scale;
     return a;
 }

@@ -317,12 +317,12 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k,
 //            (m, l, o) of each item that it does not hold whole, and a second
 //            kernel joins the partials.
 constexpr int TP = 32;        // positions per tile = one warp's step
-#ifndef KV4_NW
-#define KV4_NW 8
-#define KV4_STG 2
-#endif
-constexpr int NW = KV4_NW;    // warps per CTA, each with its own tiles and copies in flight
-constexpr int STG = KV4_STG;  // tiles in flight per warp
+// Six warps with two tiles each and two CTAs per SM: 60 to 120 KB in flight per SM.  8 x 2 tiles
+// took 10.4 us for 9.9 (16 heads over 2,300 keys, fp32) and 24.9 for 23.5 (32,768 keys, fp16);
+// 8 x 3 14.4 and 30.9 (one CTA per SM), 4 x 4 9.6 and 25.4; three CTAs of 6 warps spill: 10.7
+// and 32.0.
+constexpr int NW = 6;         // warps per CTA, each with its own tiles and copies in flight
+constexpr int STG = 2;        // tiles in flight per warp
 constexpr int MAXS = 8;       // CTAs per cluster
 
 // Both products run transposed, the cache as the 16-row operand and the query
@@ -442,6 +442,24 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t* r) {
     r[2] = (w >> 8) & 0x000F000Fu;
     r[3] = (w >> 8) & 0x00F000F0u;
 }
+// The same as normal numbers (code - SUB) * {1, 16, 1, 16}: 1024 + code comes of the bits as well,
+// and the subtraction is exact.
+template <int SUB>
+__device__ __forceinline__ void unpack4_normal(uint32_t w, uint32_t* r) {
+    constexpr uint32_t BIG = 0x64006400u;                              // 1024
+    r[0] = (w & 0x000F000Fu) | BIG;
+    r[1] = (w & 0x00F000F0u) | BIG;
+    r[2] = ((w >> 8) & 0x000F000Fu) | BIG;
+    r[3] = ((w >> 8) & 0x00F000F0u) | BIG;
+    constexpr uint32_t OFF = 0xE400E400u + SUB * 0x00010001u, OFF16 = 0xE400E400u + 16 * SUB * 0x00010001u;   // -(1024 + SUB), -(1024 + 16 SUB)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(i & 1 ? OFF16 : OFF));
+}
+template <bool NORMAL, int SUB>
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t* r) {
+    if (NORMAL) unpack4_normal<SUB>(w, r);
+    else unpack4(w, r);
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -502,6 +520,14 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
     using TL = Tile<D, NG>;
     constexpr int RT = rows_of(MODE), BLK = D / 32, BPG = BLK / NG;   // 32-channel blocks, per group
     constexpr int NT = RT / 8;                                        // tiles of 8 query rows
+    // fp32 tensors.  The matrix unit aligns products by their operands' exponents and cuts them 24
+    // bits below the largest; a subnormal counts there as 2^-14, so of products of codes as
+    // subnormals 14 to 18 bits are left, enough for 16-bit results only: here codes become
+    // normal numbers (one addition more).  And v = s (code - 8) + (z + 8 s), since over a long
+    // context sum p s code and sum p z are some 50 times what they add up to.  2,300 standard
+    // normal keys and values: off by 6e-5 of the result without both, 8e-6 without the second,
+    // 4e-7 with them, at 10.3 us for 9.9.
+    constexpr bool FINE = T == KV4_F32;
     extern __shared__ __align__(128) uint8_t smem[];
     AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
     uint8_t* const pool = smem + (sizeof(S) + 127) / 128 * 128;       // rings, then merge buffer
@@ -676,7 +702,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                 firstk[nt][e] = A.a.window > 0 && A.a.causal ? last[nt][e] - A.a.window + 1 : 0;
                 if (have) { all_lo = max(all_lo, firstk[nt][e]); all_hi = min(all_hi, last[nt][e]); }
                 // above 0: it keeps -inf
-                (e ? cq[nt].y : cq[nt].x) = fmaxf(fabsf(A.a.scale) * 1.4426950408889634f * pow2i(S.qexp[row] - 11 + 24), 1.2e-38f);
+                (e ? cq[nt].y : cq[nt].x) = fmaxf(fabsf(A.a.scale) * 1.4426950408889634f * pow2i(S.qexp[row] - 11 + (FINE ? 0 : 24)), 1.2e-38f);
             }
         }
         all_lo = __reduce_max_sync(0xffffffffu, all_lo);
@@ -749,8 +775,9 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                 for (int nt = 0; nt < NT; ++nt) {
                     float z[4];
                     mma16816_0(z, az, qz[nt], 0u);
-                    x[hh][0][nt] = make_float2(z[0] * (1.f / 65536.f), z[1] * (1.f / 65536.f));
-                    x[hh][1][nt] = make_float2(z[2] * (1.f / 65536.f), z[3] * (1.f / 65536.f));
+                    constexpr float UNIT = FINE ? 256.f : 1.f / 65536.f;
+                    x[hh][0][nt] = make_float2(z[0] * UNIT, z[1] * UNIT);
+                    x[hh][1][nt] = make_float2(z[2] * UNIT, z[3] * UNIT);
                 }
             }
 #pragma unroll
@@ -766,8 +793,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t ra[4], rb[4];
-                        unpack4(w[2 * hh].w[i2], ra);
-                        unpack4(w[2 * hh + 1].w[i2], rb);
+                        unpack<FINE, 0>(w[2 * hh].w[i2], ra);
+                        unpack<FINE, 0>(w[2 * hh + 1].w[i2], rb);
                         const uint4 a0 = make_uint4(ra[0], rb[0], ra[1], rb[1]), a1 = make_uint4(ra[2], rb[2], ra[3], rb[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -844,6 +871,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                 for (int nt = 0; nt < NT; ++nt) {
                     zl[nt][0] *= corr[nt].x;
                     zl[nt][1] *= corr[nt].y;
+                    if (FINE) { zl[nt][2] *= corr[nt].x; zl[nt][3] *= corr[nt].y; }
                     const float cx = corr[nt].x * fe, cy = corr[nt].y * fe;
 #pragma unroll
                     for (int i2 = 0; i2 < BLK; ++i2)
@@ -874,12 +902,21 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                         if (MODE == HL8) pl[k] = transpose8(pack_h2(px - h_lo(h), py - h_hi(h)));
                     }
                 {   // zeros and the row sum: rows 0..NG-1 are the groups' zeros, row NG is 1
-                    uint32_t z0 = g == NG ? 0x3C003C00u : 0u, z1 = z0;
+                    uint32_t z0 = g == NG ? 0x3C003C00u : 0u, z1 = z0, l0 = 0u, l1 = 0u;
                     if (g < NG) {
                         z0 = *reinterpret_cast<const uint32_t*>(pa + 4 * NG + 4 * g);
                         z1 = *reinterpret_cast<const uint32_t*>(pb + 4 * NG + 4 * g);
+                        if (FINE) {        // z + 8 s in two fp16 parts, the second in rows 8 ..
+                            auto centre = [](uint32_t s, uint32_t& z, uint32_t& l) {
+                                const float a = fmaf(8.f, h_lo(s), h_lo(z)), b = fmaf(8.f, h_hi(s), h_hi(z));
+                                z = pack_h2(a, b);
+                                l = pack_h2(a - h_lo(z), b - h_hi(z));
+                            };
+                            centre(*reinterpret_cast<const uint32_t*>(pa + 4 * g), z0, l0);
+                            centre(*reinterpret_cast<const uint32_t*>(pb + 4 * g), z1, l1);
+                        }
                     }
-                    const uint4 az = make_uint4(z0, 0u, z1, 0u);
+                    const uint4 az = make_uint4(z0, l0, z1, l1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma16816(zl[nt], az, ph[nt][0], ph[nt][1]);
                     if (MODE == HL8) mma16816(zl[0], az, pl[0], pl[1]);
@@ -906,8 +943,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                     const int wi = i2 >> 1;
                     const uint32_t sel = (i2 & 1) ? 0x7632u : 0x5410u;
                     uint32_t u0[4], u1[4];
-                    unpack4(__byte_perm(vw[0].w[wi], vw[1].w[wi], sel), u0);
-                    unpack4(__byte_perm(vw[2].w[wi], vw[3].w[wi], sel), u1);
+                    unpack<FINE, 8>(__byte_perm(vw[0].w[wi], vw[1].w[wi], sel), u0);
+                    unpack<FINE, 8>(__byte_perm(vw[2].w[wi], vw[3].w[wi], sel), u1);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint4 a = make_uint4(u0[2 * j], u0[2 * j + 1], u1[2 * j], u1[2 * j + 1]);
@@ -926,7 +963,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
         float* mz = mo + NW * RT * D;
         float* mm = mz + NW * RT * 8;
         {
-            const float back = pow2i(ev - 14) * 16777216.f;   // undo fv and the codes' 2^-24
+            const float back = pow2i(ev - 14) * (FINE ? 1.f : 16777216.f);   // undo fv and the codes' 2^-24
 #pragma unroll
             for (int nt8 = 0; nt8 < NT; ++nt8)
 #pragma unroll
@@ -937,7 +974,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                         *reinterpret_cast<float4*>(mo + size_t(row) * D + i * 32 + g * 4) =
                             make_float4(o[nt8][i][0][e] * back, o[nt8][i][0][2 + e] * (back * 0.0625f),
                                         o[nt8][i][1][e] * back, o[nt8][i][1][2 + e] * (back * 0.0625f));
-                    mz[row * 8 + g] = zl[nt8][e];
+                    mz[row * 8 + g] = FINE ? zl[nt8][e] + zl[nt8][2 + e] : zl[nt8][e];
                     if (g == 0) mm[row] = e ? m[nt8].y : m[nt8].x;
                 }
         }
@@ -1128,8 +1165,9 @@ cudaError_t opt_in(K* kernel, int bytes, std::atomic<uint64_t>& done) {
 // How an attention runs, by what the host knows: the mode, the row tiles and the form.
 struct Plan {
     int mode, per, nrt, nctas;
-    int64_t items, tiles;    // tiles: the most that an item can have
+    int64_t items;
     int S;                   // CTAs per item of the cluster form; 0: stream form
+    double us;               // modelled time
 };
 Plan plan_of(const Kv4Attn& a, int sms) {
     Plan p;
@@ -1140,32 +1178,37 @@ Plan plan_of(const Kv4Attn& a, int sms) {
     p.nrt = int((rows + rt - 1) / rt);
     p.nctas = sms * ctas_per_sm(p.mode, a.c.dim);
     p.items = int64_t(a.c.batch) * p.nrt * a.c.heads;
-    int64_t keys = a.c.max_ctx;
+    int64_t keys = a.c.max_ctx;                          // the most that an item can have
     if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + (rt + p.per - 1) / p.per + TP);
-    const int64_t tiles = p.tiles = (keys + TP - 1) / TP;
-    // Cluster form while a warp has few tiles: there the second launch and the list's
-    // set-up cost more than an uneven split.  2,300 keys x 16 heads: 10.1 us against
-    // 12.6 in the stream form; 32,768 x 16: 43 against 25.
-    p.S = 0;
-    if (p.items * tiles <= int64_t(p.nctas) * NW * 4) {
-        p.S = 1;
-        // clusters of 8 fill 120 of the 152 SMs with one CTA each, 288 of 304 with two
-        const int64_t room = p.nctas == sms ? p.nctas * 3 / 4 : p.nctas * 15 / 16;
-        while (p.S < MAXS && p.S * NW < tiles && p.items * p.S * 2 <= room) p.S *= 2;
+    const int64_t tiles = (keys + TP - 1) / TP;
+    // Cluster form: waves of items, each a start and an end and its warps' tiles in turn.
+    // Stream form: evenly cut tiles, but a second launch and an end for each item that a CTA
+    // works on; for few items only.  Measured at 128 channels (cluster / stream, us): 16 heads
+    // over 2,300 keys fp32 10.4 / 11.9; 8 x 8 over 8,191 bf16 20 / 24; 8 over 32,768 fp32 39 /
+    // 20, 8 x 16 125 / 108; 4 rows of 4 heads to each of 8 x 8 over 8,191 60 / 39.  More items
+    // than CTAs: 1,024 over 2,300 101 / 124, 512 over 32,768 729 / 683.
+    p.S = 1;
+    // clusters of 8 fill 120 of the 152 SMs with one CTA each, 288 of 304 with two
+    const int64_t room = p.nctas == sms ? p.nctas * 3 / 4 : p.nctas * 15 / 16;
+    while (p.S < MAXS && p.S * NW < tiles && p.items * p.S * 2 <= room) p.S *= 2;
+    const bool wide = p.mode == S16;
+    const double tile = (wide ? 1.25 : p.mode == HL8 ? 1.9 : 1.4) * a.c.dim / 128;
+    const double cluster = double((p.items * p.S + p.nctas - 1) / p.nctas) * ((wide ? 6.0 : 5.0) + tile * double((tiles + p.S * NW - 1) / (p.S * NW)));
+    const double stream = 6.0 + (wide ? 11.0 : 5.0) * (1.0 + double(p.items) / p.nctas) + tile * double(p.items) * double(tiles) / (p.nctas * NW);
+    p.us = cluster;
+    if (p.items <= p.nctas && stream < cluster) {
+        p.S = 0;
+        p.us = stream;
     }
     return p;
 }
 
-// Whether the kernel of 256-row tiles (kie_kv4_chunk.cu) takes the call: where its
-// modelled time is the smaller, from the same bound on the keys.  Here a 16-row, 32-key
-// unit takes 1.75 ns of the whole GPU after 6 us.  Measured at 128 channels, group 64
-// (rows: this / that): 8 x 16 heads over 4,096 keys 16: 37 / 53 us, 64: 113 / 53; 8 heads
-// over 32,768 keys 32: 33 / 38, 128: 83 / 45; 8 heads over 4,096 keys 64: 13 / 22, 512:
-// 60 / 45.
+// Whether the kernel of 256-row tiles (kie_kv4_chunk.cu) takes the call: where its modelled
+// time is the smaller.  Measured at 128 channels, group 64 (rows: this / that): 8 x 16 heads
+// over 4,096 keys 16: 42 / 52 us, 64: 136 / 54; 8 heads over 32,768 keys 32: 38 / 39, 128:
+// 105 / 45; 8 heads over 4,096 keys 64: 21 / 23, 512: 71 / 46.
 bool many_tokens(const Kv4Attn& a, int sms) {
-    if (a.type != KV4_BF16 || int64_t(a.n_q) * (a.heads / a.c.heads) <= 16) return false;
-    const Plan p = plan_of(a, sms);
-    return 6.0 + 1.75e-3 * double(p.items) * double(p.tiles) * a.c.dim / 128 > kie_kv4_chunk_us(&a, sms);
+    return a.type == KV4_BF16 && int64_t(a.n_q) * (a.heads / a.c.heads) > 16 && plan_of(a, sms).us > kie_kv4_chunk_us(&a, sms);
 }
 
 template <int D, int NG, int MODE, int T>

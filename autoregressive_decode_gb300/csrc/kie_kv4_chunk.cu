@@ -657,7 +657,7 @@ extern "C" double kie_kv4_chunk_us(const Kv4Attn* a, int sms) {
     const ChunkPlan p = plan_of(*a, sms);
     const bool one = int64_t(a->n_q) * p.per <= 128;
     const double rounds = double((p.items * p.nsplit + sms - 1) / sms), tiles = double((p.tiles + p.nsplit - 1) / p.nsplit);
-    return 18.0 + rounds * tiles * (one ? 1.1 : 2.2) * (a->c.dim == 64 ? 0.7 : 1.0) + (p.nsplit > 1 ? 0.5 * p.nsplit : 0.0);
+    return 18.0 + rounds * tiles * (one ? 1.1 : 2.2) * (a->c.dim == 64 ? 0.7 : 1.0) + (p.nsplit > 1 ? (one ? 0.0 : 12.0) + 0.5 * p.nsplit : 0.0);
 }
 
 extern "C" size_t kie_kv4_chunk_ws_floats(const Kv4Attn* a, int sms) {

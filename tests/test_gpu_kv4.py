@@ -319,3 +319,15 @@ def test_many_tokens_over_a_long_cache(dim, group, heads, kv_heads, n_q, window)
     assert torch.isfinite(out[0]).all()
     again = cache.attention(q, i32(*lens), n_tok=i32(*news), window=window)
     assert torch.equal(out[0], again[0])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [3, 40, 200])
+def test_window_of_the_largest_number(dtype, n):
+    """A window of 2^31 - 1 is no window, also for queries before the first key."""
+    b, hkv, hq, dim, ctx = 2, 2, 16, 128, 150
+    c = kie.KV4Cache(b, hkv, ctx, dim)
+    k, v, q = gen((b, ctx, hkv, dim), 1, dtype), gen((b, ctx, hkv, dim), 2, dtype), gen((b, n, hq, dim), 3, dtype)
+    c.append(k, v, torch.zeros(b, dtype=torch.int32, device="cuda"))
+    lens = torch.tensor([2, 130], dtype=torch.int32, device="cuda")
+    assert torch.equal(c.attention(q, lens, window=2 ** 31 - 1), c.attention(q, lens))
