@@ -520,13 +520,15 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
     using TL = Tile<D, NG>;
     constexpr int RT = rows_of(MODE), BLK = D / 32, BPG = BLK / NG;   // 32-channel blocks, per group
     constexpr int NT = RT / 8;                                        // tiles of 8 query rows
-    // fp32 tensors.  The matrix unit aligns products by their operands' exponents and cuts them 24
+    // fp32 tensors.  The matrix unit aligns what it adds by the operands' exponents and cuts it 24
     // bits below the largest; a subnormal counts there as 2^-14, so of products of codes as
     // subnormals 14 to 18 bits are left, enough for 16-bit results only: here codes become
-    // normal numbers (one addition more).  And v = s (code - 8) + (z + 8 s), since over a long
-    // context sum p s code and sum p z are some 50 times what they add up to.  2,300 standard
-    // normal keys and values: off by 6e-5 of the result without both, 8e-6 without the second,
-    // 4e-7 with them, at 10.3 us for 9.9.
+    // normal numbers (one addition more).  Then v = s (code - 8) + (z + 8 s), since over a long
+    // context sum p s code and sum p z are some 50 times what they add up to; and only the sums
+    // of 16 positions are the matrix unit's, rounded sums of those the rest.  Off, of standard
+    // normal keys and values: 6e-5 of the result at 2,300 without the three, 8e-6 without the
+    // second, 4e-7 with both; at 65,536 8e-6 without the third, 5e-7 with it, as fp32 sums in
+    // any order are.  2,300 keys take 10.6 us for 9.9.
     constexpr bool FINE = T == KV4_F32;
     extern __shared__ __align__(128) uint8_t smem[];
     AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
@@ -917,9 +919,17 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                         }
                     }
                     const uint4 az = make_uint4(z0, l0, z1, l1);
+                    if (FINE) {
+                        float f[4], low[4];
+                        mma16816_0(f, az, ph[0][0], ph[0][1]);
+                        mma16816_0(low, az, pl[0], pl[1]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(zl[nt], az, ph[nt][0], ph[nt][1]);
-                    if (MODE == HL8) mma16816(zl[0], az, pl[0], pl[1]);
+                        for (int k = 0; k < 4; ++k) zl[0][k] += f[k] + low[k];
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(zl[nt], az, ph[nt][0], ph[nt][1]);
+                        if (MODE == HL8) mma16816(zl[0], az, pl[0], pl[1]);
+                    }
                 }
                 const Words<NG> sa = load_words<NG>(pa), sb2 = load_words<NG>(pb);
                 Words<D / 64> vw[4];
@@ -948,9 +958,18 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint4 a = make_uint4(u0[2 * j], u0[2 * j + 1], u1[2 * j], u1[2 * j + 1]);
+                        if (FINE) {
+                            float f[4];
+                            mma16816_0(f, a, b[0][0], b[0][1]);
+                            mma16816(f, a, bl[0], bl[1]);
+                            float* const oo = o[0][i2][j];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i2][j], a, b[nt][0], b[nt][1]);
-                        if (MODE == HL8) mma16816(o[0][i2][j], a, bl[0], bl[1]);
+                            for (int k = 0; k < 4; ++k) oo[k] += f[k];
+                        } else {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i2][j], a, b[nt][0], b[nt][1]);
+                            if (MODE == HL8) mma16816(o[0][i2][j], a, bl[0], bl[1]);
+                        }
                     }
                 }
             }

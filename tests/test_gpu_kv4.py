@@ -331,3 +331,20 @@ def test_window_of_the_largest_number(dtype, n):
     c.append(k, v, torch.zeros(b, dtype=torch.int32, device="cuda"))
     lens = torch.tensor([2, 130], dtype=torch.int32, device="cuda")
     assert torch.equal(c.attention(q, lens, window=2 ** 31 - 1), c.attention(q, lens))
+
+
+@pytest.mark.parametrize("dim,n", [(64, 100), (128, 2300), (128, 40000)])
+def test_fp32_stays_fp32_over_long_contexts(dim, n):
+    """A probability carries a few 2^-22 (scores and their splits, exp, the split of
+    p s), a sum of 16 terms 2^-22 of the largest; all independent from key to key, so
+    over n keys they add up like the result itself, as the root of n, and stay within
+    2^-19 of its norm.  (What is cut to one side would grow with n against it.)"""
+    h = 4
+    c = kie.KV4Cache(1, h, n, dim)
+    q, k, v = gen((1, 1, h, dim), 1, "fp32"), gen((1, n, h, dim), 2, "fp32"), gen((1, n, h, dim), 3, "fp32")
+    zero, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), n, dtype=torch.int32, device="cuda")
+    c.append(k, v, zero)
+    kk, vv = (x[0].double() for x in c.read(zero, n, dtype=torch.float32))
+    p = torch.softmax(torch.einsum("hd,nhd->hn", q[0, 0].double(), kk) * dim ** -0.5, -1)
+    ref = torch.einsum("hn,nhd->hd", p, vv)
+    assert (c.attention(q, lens)[0, 0].double() - ref).norm() <= 2.0 ** -19 * ref.norm()
