@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
     constexpr bool FINE = T == KV4_F32;
     extern __shared__ __align__(128) uint8_t smem[];
     AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
-    uint8_t* const pool = smem + (sizeof(S) + 127) / 128 * 128;       // rings, then merge buffer
+    uint8_t* const pool = smem + (sizeof(S) + 127) / 128 * 128;       // rings; then every warp's sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t* ring = pool + warp * (STG * TL::BYTES);
     const uint32_t ring_u = smem_u32(ring);
@@ -730,7 +730,63 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
             }
         }
 
-        int st = 0;
+        // Every warp's (o, z and l, m) so far: [warp][RT][D], [warp][RT][8], [warp][RT].  What the
+        // matrix unit cuts off its sums is cut to one side, so they move there after FLUSH tiles
+        // (fp32 tensors' are rounded sums already).  262,144 normal keys and values, without
+        // and with it: fp16 3.5e-3 / 5e-4 of the result off, bf16 3.3e-3 / 1.9e-3.  8 x 16
+        // heads over 32,768, bf16: 110 us without, 111 at 32, 113 at 16; fp16 16 heads 23.4, 24.2 at 8.
+        constexpr int FLUSH = MODE == HL8 ? 8 : 32;
+        float* const mo = reinterpret_cast<float*>(pool + NW * STG * TL::BYTES);
+        float* const mz = mo + NW * RT * D;
+        float* const mm = mz + NW * RT * 8;
+        bool flushed = false;
+        auto flush = [&]() {
+            const float back = pow2i(ev - 14) * (FINE ? 1.f : 16777216.f);   // undo fv and the codes' 2^-24
+            float f[NT][2];
+#pragma unroll
+            for (int nt8 = 0; nt8 < NT; ++nt8)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float old = flushed ? mm[warp * RT + nt8 * 8 + 2 * t + e] : -INFINITY;
+                    f[nt8][e] = old == -INFINITY ? 0.f : ex2(old - (e ? m[nt8].y : m[nt8].x));
+                }
+            __syncwarp();
+#pragma unroll
+            for (int nt8 = 0; nt8 < NT; ++nt8)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = warp * RT + nt8 * 8 + 2 * t + e;
+#pragma unroll
+                    for (int i = 0; i < BLK; ++i) {
+                        float4* const at = reinterpret_cast<float4*>(mo + size_t(row) * D + i * 32 + g * 4);
+                        float4 v = make_float4(o[nt8][i][0][e] * back, o[nt8][i][0][2 + e] * (back * 0.0625f),
+                                               o[nt8][i][1][e] * back, o[nt8][i][1][2 + e] * (back * 0.0625f));
+                        if (flushed) {
+                            const float4 w = *at;
+                            v.x = fmaf(f[nt8][e], w.x, v.x);
+                            v.y = fmaf(f[nt8][e], w.y, v.y);
+                            v.z = fmaf(f[nt8][e], w.z, v.z);
+                            v.w = fmaf(f[nt8][e], w.w, v.w);
+                        }
+                        *at = v;
+                    }
+                    const float z = FINE ? zl[nt8][e] + zl[nt8][2 + e] : zl[nt8][e];
+                    mz[row * 8 + g] = flushed ? fmaf(f[nt8][e], mz[row * 8 + g], z) : z;
+                    if (g == 0) mm[row] = e ? m[nt8].y : m[nt8].x;
+                }
+#pragma unroll
+            for (int nt8 = 0; nt8 < NT; ++nt8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    zl[nt8][k] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < BLK; ++i) o[nt8][i][0][k] = o[nt8][i][1][k] = 0.f;
+                }
+            flushed = true;
+            __syncwarp();
+        };
+
+        int st = 0, kept = 0;
         for (int i = warp; i < ntile; i += NW) {
             {
                 const int nx = i + (STG - 1) * NW;
@@ -739,6 +795,10 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                 __syncwarp();          // every lane is done with the stage that this overwrites
                 if (nx < ntile) copy_tile(nx, ns);
                 cp_async_commit();
+            }
+            if (!FINE && kept++ == FLUSH) {
+                flush();
+                kept = 1;
             }
             cp_async_wait_group<STG - 1>();
             __syncwarp();
@@ -974,29 +1034,9 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                 }
             }
         }
+        // ---- merge the warps
         cp_async_wait_group<0>();
-        __syncthreads();               // every warp is done with its ring: it becomes the merge buffer
-
-        // ---- merge the warps: [warp][RT][D] sums, [warp][RT][8] zeros and row sums, [warp][RT] maxima
-        float* mo = reinterpret_cast<float*>(pool);
-        float* mz = mo + NW * RT * D;
-        float* mm = mz + NW * RT * 8;
-        {
-            const float back = pow2i(ev - 14) * (FINE ? 1.f : 16777216.f);   // undo fv and the codes' 2^-24
-#pragma unroll
-            for (int nt8 = 0; nt8 < NT; ++nt8)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = warp * RT + nt8 * 8 + 2 * t + e;
-#pragma unroll
-                    for (int i = 0; i < BLK; ++i)
-                        *reinterpret_cast<float4*>(mo + size_t(row) * D + i * 32 + g * 4) =
-                            make_float4(o[nt8][i][0][e] * back, o[nt8][i][0][2 + e] * (back * 0.0625f),
-                                        o[nt8][i][1][e] * back, o[nt8][i][1][2 + e] * (back * 0.0625f));
-                    mz[row * 8 + g] = FINE ? zl[nt8][e] + zl[nt8][2 + e] : zl[nt8][e];
-                    if (g == 0) mm[row] = e ? m[nt8].y : m[nt8].x;
-                }
-        }
+        flush();
         __syncthreads();
         const bool whole = CLUSTER ? A.nctas == 1 : ntile == nt;
         float* part = A.a.ws + (size_t(pair) * c.heads + head + blockIdx.x) * (RT * (D + 2));
@@ -1080,7 +1120,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
         }
         if (CLUSTER) break;
         if (threadIdx.x == 0) S.plan[0] += ntile;
-        __syncthreads();               // the merge buffer becomes the ring again
+        __syncthreads();               // the sums have been read
     }
 }
 
@@ -1234,7 +1274,7 @@ template <int D, int NG, int MODE, int T>
 cudaError_t launch_attention(AttnArgs A, const Plan& p, cudaStream_t st) {
     constexpr int RT = rows_of(MODE);
     constexpr int ring = NW * STG * Tile<D, NG>::BYTES, merge = NW * RT * (D + 9) * 4;
-    constexpr int smem = (int(sizeof(AttnShared<D, NG, MODE>)) + 127) / 128 * 128 + (ring > merge ? ring : merge);
+    constexpr int smem = (int(sizeof(AttnShared<D, NG, MODE>)) + 127) / 128 * 128 + ring + merge;
     static std::atomic<uint64_t> done{0}, done_c{0};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];

@@ -348,3 +348,18 @@ def test_fp32_stays_fp32_over_long_contexts(dim, n):
     p = torch.softmax(torch.einsum("hd,nhd->hn", q[0, 0].double(), kk) * dim ** -0.5, -1)
     ref = torch.einsum("hn,nhd->hd", p, vv)
     assert (c.attention(q, lens)[0, 0].double() - ref).norm() <= 2.0 ** -19 * ref.norm()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_16_bit_results_over_long_contexts(dtype):
+    """The result's own rounding, at most half a step for each element, and as much
+    again for p's and the sums', over so many keys that each warp adds many tiles."""
+    h, dim, n = 1, 128, 600000
+    c = kie.KV4Cache(1, h, n, dim, 128)
+    q, k, v = gen((1, 1, h, dim), 1, dtype), gen((1, n, h, dim), 2, dtype), gen((1, n, h, dim), 3, dtype)
+    zero, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), n, dtype=torch.int32, device="cuda")
+    c.append(k, v, zero)
+    kk, vv = (x[0].double() for x in c.read(zero, n, dtype=torch.float32))
+    p = torch.softmax(torch.einsum("hd,nhd->hn", q[0, 0].double(), kk) * dim ** -0.5, -1)
+    ref = torch.einsum("hn,nhd->hd", p, vv)
+    assert (c.attention(q, lens)[0, 0].double() - ref).norm() <= torch.finfo(TYPES[dtype]).eps * ref.norm()
