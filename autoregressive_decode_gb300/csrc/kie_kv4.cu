@@ -195,52 +195,73 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const RowArgs A, const 
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
         if (!__any_sync(0xffffffffu, ok[u])) continue;
-        // saturated to +-65504, NaN as 0
-        const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), bottom = __half2half2(__ushort_as_half(0xFBFF));
-        __half2 lo2 = top, hi2 = bottom;
+        // (minimum, -maximum) of the group; NaN where there is one
+        auto extremes = [&]() {
+            __half2 lo2 = x[u][0], hi2 = x[u][0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t bits = *reinterpret_cast<uint32_t*>(&x[u][i]) & __heq2_mask(x[u][i], x[u][i]);
-            x[u][i] = __hmax2(__hmin2(*reinterpret_cast<__half2*>(&bits), top), bottom);
-            lo2 = __hmin2(lo2, x[u][i]);
-            hi2 = __hmax2(hi2, x[u][i]);
+            for (int i = 1; i < 4; ++i) {
+                lo2 = __hmin2_nan(lo2, x[u][i]);
+                hi2 = __hmax2_nan(hi2, x[u][i]);
+            }
+            hi2 = __hneg2(hi2);
+            __half2 r = __hmin2_nan(__lows2half2(lo2, hi2), __highs2half2(lo2, hi2));
+#pragma unroll
+            for (int o = 1; o < LPG; o <<= 1) r = __hmin2_nan(r, __shfl_xor_sync(0xffffffffu, r, o));
+            return r;
+        };
+        __half2 mm = extremes();
+        float lo = __low2float(mm), span = -__high2float(mm) - lo;
+        if (__any_sync(0xffffffffu, !(span <= 131008.f))) {      // infinities and NaN: saturated to +-65504, as 0
+            const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), bottom = __half2half2(__ushort_as_half(0xFBFF));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t bits = *reinterpret_cast<uint32_t*>(&x[u][i]) & __heq2_mask(x[u][i], x[u][i]);
+                x[u][i] = __hmax2(__hmin2(*reinterpret_cast<__half2*>(&bits), top), bottom);
+            }
+            mm = extremes();
+            lo = __low2float(mm);
+            span = -__high2float(mm) - lo;
         }
-        // (minimum, -maximum) of the lane, then of the group: one exchange per step
-        __half2 mm = __hmin2(__lows2half2(lo2, __hneg2(hi2)), __highs2half2(lo2, __hneg2(hi2)));
-#pragma unroll
-        for (int o = 1; o < LPG; o <<= 1) mm = __hmin2(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-        const float lo = __low2float(mm), hi = -__high2float(mm);
-        const __half sh = __float2half_rn(div15(hi - lo));
+        const __half sh = __float2half_rn(div15(span));
         const float sf = __half2float(sh);
         float rcp;                   // 0 for a constant group: all codes 0
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(sf));
         if (!(sf > 0.f)) rcp = 0.f;
-        // code = rint((x - z) / s), at most 15: by the reciprocal, which is within 2^-18 of
-        // the quotient, so only a value that close to a half needs the division itself.
-        // Adding 1.5 * 2^23 rounds to even and leaves the code in the low bits.
+        // code = rint((x - z) / s): by the reciprocal, which is within 2^-18 of the quotient, so
+        // only a value that close to a half needs the division itself.  Adding 1.5 * 2^23 rounds
+        // to even.  A normal s is within 2^-11 of its quotient and the codes end at 15; a
+        // subnormal one's are limited.
         constexpr float MAGIC = 12582912.f;
-        float d[8], c8[8], far = 0.f;
+        const float2 magic = make_float2(MAGIC, MAGIC), rcp2 = make_float2(rcp, rcp), neg = make_float2(-lo, -lo);
+        float2 d[4], n[4];           // n: codes, negated
+        float far = 0.f;             // largest distance from a code
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            d[i] = (i & 1 ? __high2float(x[u][i >> 1]) : __low2float(x[u][i >> 1])) - lo;
-            c8[i] = fmaf(d[i], rcp, MAGIC);
-            far = fmaxf(far, fabsf(fmaf(d[i], rcp, -(c8[i] - MAGIC))));     // largest distance from a code
+        for (int i = 0; i < 4; ++i) {
+            d[i] = __fadd2_rn(__half22float2(x[u][i]), neg);
+            n[i] = __ffma2_rn(__ffma2_rn(d[i], rcp2, magic), make_float2(-1.f, -1.f), magic);
+            const float2 e = __ffma2_rn(d[i], rcp2, n[i]);
+            far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
         }
-        if (far > 0.5f - 1.f / 65536.f) {
+        if (far > 0.5f - 1.f / 65536.f || (sf < 6.103515625e-5f && sf > 0.f)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c8[i] = rintf(__fdiv_rn(d[i], sf)) + MAGIC;
+            for (int i = 0; i < 4; ++i) {
+                n[i].x = -fminf(rintf(__fdiv_rn(d[i].x, sf)), 15.f);
+                n[i].y = -fminf(rintf(__fdiv_rn(d[i].y, sf)), 15.f);
+            }
         }
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 7; i >= 0; --i) word = word * 16u + (__float_as_uint(fminf(c8[i], MAGIC + 15.f)) & 15u);
+        // sum of code_i 16^i, in two halves of 16 bits
+        const float2 b256 = make_float2(256.f, 256.f);
+        const float2 w0 = __ffma2_rn(n[1], b256, n[0]), w1 = __ffma2_rn(n[3], b256, n[2]);
+        const uint32_t word = __byte_perm(__float_as_uint(fmaf(w0.y, -16.f, MAGIC - w0.x)),
+                                          __float_as_uint(fmaf(w1.y, -16.f, MAGIC - w1.x)), 0x5410);
         if (!isv) {
             if (ok[u]) reinterpret_cast<uint32_t*>(c.kc)[row[u] * LPR + (l & 3) * BLK + (l >> 2)] = word;
         } else {
             // lane l stores word l = units (g, 2wi) and (g, 2wi + 1): see kie_kv4.h
             const int g = l / (D / 64), wi = l % (D / 64);
             const int src = (lane - l) + 8 * wi + (g >> 1);
-            const uint32_t w0 = __shfl_sync(0xffffffffu, word, src), w1 = __shfl_sync(0xffffffffu, word, src + 4);
-            if (ok[u]) reinterpret_cast<uint32_t*>(c.vc)[row[u] * LPR + l] = __byte_perm(w0, w1, (g & 1) ? 0x7632 : 0x5410);
+            const uint32_t v0 = __shfl_sync(0xffffffffu, word, src), v1 = __shfl_sync(0xffffffffu, word, src + 4);
+            if (ok[u]) reinterpret_cast<uint32_t*>(c.vc)[row[u] * LPR + l] = __byte_perm(v0, v1, (g & 1) ? 0x7632 : 0x5410);
         }
         if (ok[u] && l % LPG == 0) {
             const ParAt at = par_at(row[u], l / LPG, NG, isv);
@@ -282,11 +303,17 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k,
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
         if (ok[u]) {
-            const float2 p = h2_to_f2(sz[u]);
+            const float2 p = h2_to_f2(sz[u]), ps = make_float2(p.x, p.x), pz = make_float2(p.y, p.y);
+            const uint32_t even = word[u] & 0x0F0F0F0Fu, odd = (word[u] >> 4) & 0x0F0F0F0Fu;
             float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = fmaf(__uint_as_float(((word[u] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f, p.x, p.y);
+            for (int i = 0; i < 4; ++i) {      // 2^23 + code comes of the bits
+                const float2 big = make_float2(__uint_as_float(__byte_perm(even, 0x4B000000u, 0x7540 + i)),
+                                               __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7540 + i)));
+                const float2 y = __ffma2_rn(__fadd2_rn(big, make_float2(-8388608.f, -8388608.f)), ps, pz);
+                f[2 * i] = y.x;
+                f[2 * i + 1] = y.y;
+            }
             E* q = base + w.t * st.t + w.h * st.h;
             if (T == KV4_F16) {
                 uint4 o;
