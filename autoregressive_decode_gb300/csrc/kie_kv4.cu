@@ -397,6 +397,11 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k,
 //            one per CTA, whatever the requests' lengths; a CTA leaves a partial
 //            (m, l, o) of each item that it does not hold whole, and a second
 //            kernel joins the partials.
+// Long contexts are bound by memory: 8 requests x 16 heads over 32,768 keys, bf16 (671 MB)
+// 111 us, 0.89 of the copy rate; there the integer pipe, which takes the codes apart, is
+// half busy.  Short ones by latency: an item's chain (lengths, queries, first tiles, the
+// join) is 4 us, a second launch 5 more.  16 heads over 32,768 keys in fp16 24 us (floor 11), 8
+// ragged requests of up to 8,191 keys 19 (6), 16 heads over 2,300 in fp32 9.9 (0.9).
 constexpr int TP = 32;        // positions per tile = one warp's step
 // Six warps with two tiles each and two CTAs per SM: 60 to 120 KB in flight per SM.  8 x 2 tiles
 // took 10.4 us for 9.9 (16 heads over 2,300 keys, fp32) and 24.9 for 23.5 (32,768 keys, fp16);
@@ -602,7 +607,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
     // of 16 positions are the matrix unit's, rounded sums of those the rest.  Off, of standard
     // normal keys and values: 6e-5 of the result at 2,300 without the three, 8e-6 without the
     // second, 4e-7 with both; at 65,536 8e-6 without the third, 5e-7 with it, as fp32 sums in
-    // any order are.  2,300 keys take 10.6 us for 9.9.
+    // any order are.  They took 2,300 keys from 9.9 to 10.6 us (9.8 since a warp's sums have
+    // memory of their own).
     constexpr bool FINE = T == KV4_F32;
     extern __shared__ __align__(128) uint8_t smem[];
     AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
