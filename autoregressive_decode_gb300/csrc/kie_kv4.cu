@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k,
 // 111 us, 0.89 of the copy rate; there the integer pipe, which takes the codes apart, is
 // half busy.  Short ones by latency: an item's chain (lengths, queries, first tiles, the
 // join) is 4 us, a second launch 5 more.  16 heads over 32,768 keys in fp16 24 us (floor 11), 8
-// ragged requests of up to 8,191 keys 19 (6), 16 heads over 2,300 in fp32 9.9 (0.9).
+// ragged requests of up to 8,191 keys 19 (6), 16 heads over 2,300 in fp32 10.0 (0.9).
 constexpr int TP = 32;        // positions per tile = one warp's step
 // Six warps with two tiles each and two CTAs per SM: 60 to 120 KB in flight per SM.  8 x 2 tiles
 // took 10.4 us for 9.9 (16 heads over 2,300 keys, fp32) and 24.9 for 23.5 (32,768 keys, fp16);
@@ -602,13 +602,13 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
     // fp32 tensors.  The matrix unit aligns what it adds by the operands' exponents and cuts it 24
     // bits below the largest; a subnormal counts there as 2^-14, so of products of codes as
     // subnormals 14 to 18 bits are left, enough for 16-bit results only: here codes become
-    // normal numbers (one addition more).  Then v = s (code - 8) + (z + 8 s), since over a long
-    // context sum p s code and sum p z are some 50 times what they add up to; and only the sums
-    // of 16 positions are the matrix unit's, rounded sums of those the rest.  Off, of standard
-    // normal keys and values: 6e-5 of the result at 2,300 without the three, 8e-6 without the
-    // second, 4e-7 with both; at 65,536 8e-6 without the third, 5e-7 with it, as fp32 sums in
-    // any order are.  They took 2,300 keys from 9.9 to 10.6 us (9.8 since a warp's sums have
-    // memory of their own).
+    // normal numbers (one addition more).  Then K and V are taken as s (code - 8) + (z + 8 s),
+    // since over a long context sum p s code and sum p z are some 50 times what they add up to;
+    // and only the sums of 16 positions are the matrix unit's, rounded sums of those the rest.
+    // Off, of standard normal keys and values: 6e-5 of the result at 2,300 without the three,
+    // 8e-6 without the second, 2e-7 with both; at 65,536 8e-6 without the third, 3e-7 with it: no
+    // more than plain fp32 sums.  They took 2,300 keys from 9.9 to 10.6 us (10.0 since a warp's
+    // sums have memory of their own).
     constexpr bool FINE = T == KV4_F32;
     extern __shared__ __align__(128) uint8_t smem[];
     AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
@@ -911,12 +911,23 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
             }
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
+                // zeros of this lane's pair of groups (NG == 1: beside the scale, whose factor is 0)
                 auto zero = [&](const Words<NG>& q) { return NG == 4 ? ((t & 1) ? q.w[3 % NG] : q.w[2 % NG]) : q.w[NG - 1]; };
-                const uint4 az = make_uint4(zero(par[2 * hh]), zero(par[2 * hh + 1]), 0u, 0u);
+                uint4 az = make_uint4(zero(par[2 * hh]), zero(par[2 * hh + 1]), 0u, 0u);
+                if (FINE) {                // z + 8 s in two parts, the second at k = 8 ..
+                    auto centre = [&](const Words<NG>& q, uint32_t& z, uint32_t& low) {
+                        const uint32_t s = NG == 4 ? ((t & 1) ? q.w[1 % NG] : q.w[0]) : NG == 2 ? q.w[0] : q.w[0] << 16;
+                        const float a = NG == 1 ? 0.f : fmaf(8.f, h_lo(s), h_lo(z)), b = fmaf(8.f, h_hi(s), h_hi(z));
+                        z = pack_h2(a, b);
+                        low = pack_h2(a - h_lo(z), b - h_hi(z));
+                    };
+                    centre(par[2 * hh], az.x, az.z);
+                    centre(par[2 * hh + 1], az.y, az.w);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float z[4];
-                    mma16816_0(z, az, qz[nt], 0u);
+                    mma16816_0(z, az, qz[nt], FINE ? qz[nt] : 0u);
                     constexpr float UNIT = FINE ? 256.f : 1.f / 65536.f;
                     x[hh][0][nt] = make_float2(z[0] * UNIT, z[1] * UNIT);
                     x[hh][1][nt] = make_float2(z[2] * UNIT, z[3] * UNIT);
@@ -935,8 +946,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t ra[4], rb[4];
-                        unpack<FINE, 0>(w[2 * hh].w[i2], ra);
-                        unpack<FINE, 0>(w[2 * hh + 1].w[i2], rb);
+                        unpack<FINE, 8>(w[2 * hh].w[i2], ra);
+                        unpack<FINE, 8>(w[2 * hh + 1].w[i2], rb);
                         const uint4 a0 = make_uint4(ra[0], rb[0], ra[1], rb[1]), a1 = make_uint4(ra[2], rb[2], ra[3], rb[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -992,9 +1003,11 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                 }
                 const float2 mn = make_float2(max_nan(m[nt].x, mx.x * cq[nt].x), max_nan(m[nt].y, mx.y * cq[nt].y));
                 grew |= mn.x > m[nt].x || mn.y > m[nt].y;
-                // p <= 2^15: fp16's range, used whole
-                mref[nt] = make_float2((mn.x == -INFINITY ? 0.f : mn.x) - 15.f, (mn.y == -INFINITY ? 0.f : mn.y) - 15.f);
-                corr[nt] = make_float2(ex2(m[nt].x - 15.f - mref[nt].x), ex2(m[nt].y - 15.f - mref[nt].y));
+                // p <= 2^15: fp16's range, used whole (fp32 tensors: by a product, as exponents near
+                // 15 are rounded to 2^-21)
+                constexpr float UP = FINE ? 0.f : 15.f;
+                mref[nt] = make_float2((mn.x == -INFINITY ? 0.f : mn.x) - UP, (mn.y == -INFINITY ? 0.f : mn.y) - UP);
+                corr[nt] = make_float2(ex2(m[nt].x - UP - mref[nt].x), ex2(m[nt].y - UP - mref[nt].y));
                 m[nt] = mn;
             }
             uint32_t sb;
@@ -1038,7 +1051,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float2 y = x[hh][k][nt];
-                        const float px = ex2(fmaf(y.x, cq[nt].x, -mref[nt].x)), py = ex2(fmaf(y.y, cq[nt].y, -mref[nt].y));
+                        constexpr float UP = FINE ? 32768.f : 1.f;
+                        const float px = ex2(fmaf(y.x, cq[nt].x, -mref[nt].x)) * UP, py = ex2(fmaf(y.y, cq[nt].y, -mref[nt].y)) * UP;
                         const uint32_t h = pack_h2(px, py);
                         ph[nt][k] = transpose8(h);
                         if (MODE == HL8) pl[k] = transpose8(pack_h2(px - h_lo(h), py - h_hi(h)));

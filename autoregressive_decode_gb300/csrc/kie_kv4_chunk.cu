@@ -23,7 +23,7 @@
 // Rounding: K, V and P to fp16 (2^-12 relative on average less), 16 times finer
 // than the bf16 results this serves.
 //
-// 1,024 tokens x 32 heads of 128 at the end of 4,096 keys (60 GFLOP): 86 us, 0.70 PFLOP/s.
+// 1,024 tokens x 32 heads of 128 at the end of 4,096 keys (60 GFLOP): 89 us, 0.67 PFLOP/s.
 // The matrix unit's own time there is 45 us (51 cycles an instruction for S, 65 for P V), 68
 // us with everything else taken out of the loop but its barriers; the softmax shares the SM
 // with the conversion of the codes.  A sixth of the SMs is idle: 128 CTAs.
@@ -175,6 +175,22 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t s2, uint32_t z2) {
     r.z = hfma2(hadd2((w8 & 0x000F000Fu) | K1024, M1024), s2, z2);
     r.w = hfma2(hfma2((w8 & 0x00F000F0u) | K1024, SIXTEENTH, M64), s2, z2);
     return r;
+}
+
+// Whether code 15 of either group reaches beyond fp16 (where values as large as the type has
+// were stored and s was rounded up): an exponent of all ones in 15 s + z.
+__device__ __forceinline__ uint32_t beyond(uint32_t s2, uint32_t z2) {
+    return ((hfma2(0x4B804B80u, s2, z2) & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+// Keeps a key's values inside the type.
+template <int D>
+__device__ __forceinline__ void inside(uint8_t* dst) {
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i) {
+        uint32_t* const w = reinterpret_cast<uint32_t*>(dst + i * 128);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm("min.f16x2 %0, %0, %1;" : "+r"(w[j]) : "r"(0x7BFF7BFFu));
+    }
 }
 
 template <int T> struct El;
@@ -340,6 +356,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
                     *reinterpret_cast<uint4*>(dst + (bl * 4 + j) * 128) = values8(w, s2, z2);
                 }
             }
+            uint32_t wide = NG == 1 ? K.p[0] & 0xFFFFu : 0u;            // a scale of 2 or more: look closer
+#pragma unroll
+            for (int gi = 0; gi < NG / 2; ++gi) wide |= K.p[gi];
+            if (__any_sync(0xffffffffu, wide & 0x40004000u)) {
+                uint32_t far = NG == 1 ? beyond(K.p[0], K.p[0] >> 16) & 0xFFFFu : 0u;
+#pragma unroll
+                for (int gi = 0; gi < NG / 2; ++gi) far |= beyond(K.p[gi], K.p[NG / 2 + gi]);
+                if (far) inside<D>(dst);
+            }
         };
         auto put_v = [&](int i) {
             const int p = base + i * KEYS + k;
@@ -363,6 +388,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_chunk_kernel(const ChunkArgs A
                     const uint32_t w = __byte_perm(word(u0), word(u1), (u0 & 1) ? 0x7632 : 0x5410);
                     *reinterpret_cast<uint4*>(dst + (bl * 4 + j) * 128) = values8(w, s2, z2);
                 }
+            }
+            uint32_t wide = 0u;
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) wide |= V.p[gi];
+            if (__any_sync(0xffffffffu, wide & 0x40004000u)) {
+                uint32_t far = 0u;
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) far |= beyond(V.p[gi], V.p[NG + gi]);
+                if (far) inside<D>(dst);
             }
         };
         // the tile that used the same stage last is done with it: its parity

@@ -26,11 +26,11 @@
 //     one value or a few tokens are left.
 //
 // The bytes would take 0.02 us for a row of 32,000 and 4.9 us for 64 of 131,072; what
-// bounds it is, for few rows, the chain of passes and of cluster barriers (about 0.7 us
-// each with what it waits for), and for many the 45 instructions of an exact weight.
-// Measured (us; unfiltered / top-k 50 / top-p 0.9 / greedy): 1 x 32,000 fp32 8.2 / 12.9 /
-// 19.9 / 5.2; 8 x 50,001 bf16 9.6 / 14.1 / 23.7 / 5.9; 64 x 131,072 fp32 41 / 38 / 93 / 17;
-// 256 x 32,000 fp32 36 / 39 / 74 / 13.
+// bounds it is, for few rows, the chain of passes and of cluster barriers, and for many
+// the 45 instructions of an exact weight.
+// Measured (us; unfiltered / top-k 50 / top-p 0.9): 1 x 32,000 fp32 8.2 / 13.1 / 20.1 (greedy
+// 5.2); 8 x 50,001 bf16 9.6 / 14.1 / 23.7; 64 x 32,000 fp32 13 / 15 / 29; 256 x 32,000 35 / 34
+// / 71; 64 x 131,072 38 / 41 / 84 (greedy 17: what reading and the first barrier take).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,7 +51,9 @@ constexpr int NF = 4 * NB;                 // bins of the approximate masses, a 
 constexpr int FRAC = 44;                   // masses count 2^-44
 constexpr int LIST = 32;                   // candidates resolved by one warp
 constexpr int MAXC = 8;                    // CTAs per row
-constexpr int KLIM = 512, CAP = 1024;      // the sorted paths: largest top-k, most candidates
+// The sorted paths: largest top-k, most candidates.  Top-k 400 of 32,000: 15.6 us sorted, and
+// 2,000 22 by histograms.
+constexpr int KLIM = 512, CAP = 1024;
 
 // 2^(-j/128) * 2^60, by the series of exp(-j ln 2 / 128) (to 2^-52)
 struct Pow2 { uint64_t v[128]; };
@@ -959,10 +961,12 @@ cudaError_t launch_t(const SampleArgs& a, int C, int S, cudaStream_t st) {
 }  // namespace
 
 extern "C" cudaError_t kie_launch_sample(const SampleArgs* a, int sms, cudaStream_t st) {
-    // CTAs per row: enough to fill the GPU (two per SM) with few rows, and at least so
-    // many that a slice fits shared memory; a slice below 1,024 gains nothing more
+    // CTAs per row: while one per SM is left over and a slice is above 4,096, and at least
+    // so many that a slice fits shared memory.  Top-p 0.9 with 1, 2, 4, 8 CTAs a row, us:
+    // 1 x 4,000 15.1, 16.2, 15.6, 16.9; 1 x 32,000 35, 27, 21, 20; 32 x 32,000 37, 28, 22,
+    // 27; 64 x 32,000 37, 29, 28, 50; 256 x 32,000 72, 74, 93, 179.
     int C = 1;
-    while (C < MAXC && (int64_t(a->rows) * C < 2 * sms || int64_t(a->vocab) > int64_t(C) * 32768) && a->vocab > C * 1024) C *= 2;
+    while (C < MAXC && ((int64_t(a->rows) * 2 * C <= sms && a->vocab > C * 4096) || int64_t(a->vocab) > int64_t(C) * 32768)) C *= 2;
     const int S = ((a->vocab + C - 1) / C + 7) / 8 * 8;
     if (a->type == 0) return launch_t<0>(*a, C, S, st);
     if (a->type == 1) return launch_t<1>(*a, C, S, st);

@@ -363,3 +363,29 @@ def test_16_bit_results_over_long_contexts(dtype):
     p = torch.softmax(torch.einsum("hd,nhd->hn", q[0, 0].double(), kk) * dim ** -0.5, -1)
     ref = torch.einsum("hn,nhd->hd", p, vv)
     assert (c.attention(q, lens)[0, 0].double() - ref).norm() <= torch.finfo(TYPES[dtype]).eps * ref.norm()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1, 100])
+def test_values_at_the_end_of_fp16(dtype, n):
+    """Values stored at +-65504 (infinities among them) round to 65,536 with their
+    scale: finite results for one token and for many."""
+    b, hkv, hq, dim, ctx = 1, 2, 8, 128, 200
+    c = kie.KV4Cache(b, hkv, ctx, dim, 64)
+    k, v, q = gen((b, ctx, hkv, dim), 1, dtype), gen((b, ctx, hkv, dim), 2, dtype), gen((b, n, hq, dim), 3, dtype)
+    v[0, ::7, :, 3] = math.inf
+    v[0, ::7, :, 5] = -math.inf
+    v[0, 3::11, :, 70] = 65504.0
+    v[0, 3::11, :, 71] = -65504.0
+    lens = torch.full((b,), ctx, dtype=torch.int32, device="cuda")
+    c.append(k, v, torch.zeros(b, dtype=torch.int32, device="cuda"))
+    check(c.attention(q, lens), q, stored(k, 64), stored(v, 64), [ctx], [n], dtype)
+    # the greatest key alone decides
+    k[0, 50] = math.inf
+    k[0, 50, :, 1] = -math.inf
+    q[..., :] = 1.0
+    c.append(k, v, torch.zeros(b, dtype=torch.int32, device="cuda"))
+    out = c.attention(q, lens, causal=False)
+    want = stored(v, 64)[0, 50].repeat(hq // hkv, 0)
+    # p s code and p z, each at most 3 of the largest |v| together, with p s rounded by 2^-11 twice
+    assert np.allclose(out[0, -1].double().cpu().numpy(), want, rtol=2.0 ** -8, atol=6 * 2.0 ** -11 * np.abs(want).max())
