@@ -85,13 +85,11 @@ struct Shared {
     // result of find()
     int32_t f_bin;
     uint32_t f_cnt, f_n;
-    uint64_t f_mass, f_m;
+    uint64_t f_mass;
     // result of select()
     uint32_t key, n_eq, all_eq, last;
     uint64_t mass;
     float chi, clo;
-    int32_t token;
-    uint64_t token_w;
 };
 
 template <int T> __device__ __forceinline__ float to_float(const void* p, int64_t i);
@@ -405,7 +403,6 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
                 sh.f_cnt = cb;
                 sh.f_mass = mb;
                 sh.f_n = cj;
-                sh.f_m = mj;
             }
             cb += cj;
             mb += mj;

@@ -444,7 +444,8 @@ kie_status kie_kv4_read(const kie_kv4_cache* c, void* k, void* v, int32_t dtype,
  * window > 0 only the last `window` of them; not causal: all kv_len[b] (window
  * must be 0).  A query that sees no key gives zeros.  out = softmax(scale q k^T)
  * v over the values that the cache stands for; scores, softmax and sums in
- * fp32.  scale must be finite.  Waits inside the kernels are bounded (2 s); rows
+ * fp32 (of bf16 tensors p, and with many query rows K and V too, are rounded to
+ * fp16 for the products).  scale must be finite.  Waits inside the kernels are bounded (2 s); rows
  * whose wait ran out are NaN. */
 typedef struct {
     const void* q;
