@@ -160,6 +160,21 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
     return v;
 }
 
+// x 2^bits, 0 <= x <= 1, rounded down (or up); without fp64, whose unit serves two lanes a cycle.
+__device__ __forceinline__ uint64_t fixed(float x, int bits, bool up) {
+    const uint32_t b = __float_as_uint(x), e = max(b >> 23, 1u), m = b >> 23 ? (b & 0x7FFFFFu) | 0x800000u : b;
+    const int shift = int(e) - 150 + bits;
+    if (shift >= 0) return uint64_t(m) << shift;
+    if (shift < -24) return up && m ? 1ull : 0ull;
+    return (m + (up ? (1u << -shift) - 1u : 0u)) >> -shift;
+}
+// w / total <= 1 to fp32's rounding: the quotient of both rounded, and what the roundings left.
+__device__ __forceinline__ float ratio(uint64_t w, uint64_t total) {
+    const float fw = __ull2float_rn(w), ft = __ull2float_rn(total), q = fw / ft;
+    const float rw = __ll2float_rn(int64_t(w - __float2ull_rn(fw))), rt = __ll2float_rn(int64_t(total - __float2ull_rn(ft)));
+    return q + (fmaf(-q, ft, fw) + fmaf(-q, rt, rw)) / ft;
+}
+
 // Bin of y: its sixteenths, rounded down (the addition of 2^23 does that), the last
 // bin for all from 1023 / 16 on (and for NaN, an infinite distance at an infinite T).
 __device__ __forceinline__ int bin_of(float y) {
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
     const bool use_k = top_k > 0 && top_k < A.vocab, use_p = top_p < 1.f;
 
     const float min_p = A.min_p ? A.min_p[row] : 0.f;
-    const uint64_t wmin = min_p > 0.f ? uint64_t(ceil(double(fminf(min_p, 1.f)) * double(1ull << FRAC))) : 0ull;
+    const uint64_t wmin = min_p > 0.f ? fixed(fminf(min_p, 1.f), FRAC, true) : 0ull;
     // warp `warp` holds elements [i0, i1) of the slice where order matters
     const int per = (n + NWARP * 32 - 1) / (NWARP * 32) * 32;
     const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
             while (shift < 22 && ((hi - lo) >> shift) >= NB) ++shift;
             auto here = [&](float l) {
                 const uint32_t k = key_of<T>(l);
-                if (level == 0 ? bin_of(R.y(l)) != b : k < lo || k > hi) return -1;
+                if (bin_of(R.y(l)) != b || (level > 0 && (k < lo || k > hi))) return -1;   // the keys reach over the bin's ends
                 return int(min((hi - min(k, hi)) >> shift, uint32_t(NB - 1)));
             };
             histogram(1, here, std::false_type());
@@ -503,17 +518,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const SampleArgs A, const
     };
 
     const float uf = A.u[row];
-    const uint64_t U = uf >= 1.f ? ~0ull : uf > 0.f ? uint64_t(double(uf) * 18446744073709551616.0) : 0ull;
+    const uint64_t U = uf >= 1.f ? ~0ull : uf > 0.f ? fixed(uf, 64, false) : 0ull;
     // the least mass that is at least p of `mass`, and at least one token's
     auto p_target = [&](uint64_t mass) {
-        const uint64_t P = top_p > 0.f ? uint64_t(double(top_p) * 18446744073709551616.0) : 0ull;
+        const uint64_t P = top_p > 0.f ? fixed(top_p, 64, false) : 0ull;
         const uint64_t t = __umul64hi(mass, P) + (mass * P != 0ull ? 1ull : 0ull);
         return t ? t : 1ull;
     };
     auto choose = [&](int token, uint64_t w, uint64_t total) {
         A.tokens[row] = token;
         if (A.next) A.next[row] = token;
-        if (A.probs) A.probs[row] = float(double(w) / double(total));
+        if (A.probs) A.probs[row] = ratio(w, total);
     };
     // Where the running sum of val(bin, words summed over the cluster) over the bins of the
     // single-word histogram `hist` reaches the targets aim(sum of all): the bins go to f_bin

@@ -112,6 +112,18 @@ def test_near_equal_logits():
     run_and_check(x, [0.1, 0.9, 0.5, 0.3], p=[0.3, 0.5, 0.7, 0.2])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_prefix_ends_near_zero(dtype):
+    """Logits around zero, where neighbouring numbers are many: the prefix ends just
+    inside a bin that spans zero, and its keys reach into the bin before."""
+    rows, vocab = 76, 8200
+    g = np.random.default_rng(8)
+    x = logits(rows, vocab, 4, dtype, std=0.01)
+    for p in (None, 0.85, 0.9, 0.97):
+        run_and_check(x, g.random(rows), k=g.integers(2000, 6000, rows), p=p)
+    run_and_check(x, g.random(rows), p=g.uniform(0.3, 0.99, rows))
+
+
 def test_masks_and_extremes():
     v = 3000
     inf, low = math.inf, torch.finfo(torch.float32).min
