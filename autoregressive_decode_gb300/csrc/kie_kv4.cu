@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowArgs A, void* k,
 // 111 us, 0.89 of the copy rate; there the integer pipe, which takes the codes apart, is
 // half busy.  Short ones by latency: an item's chain (lengths, queries, first tiles, the
 // join) is 4 us, a second launch 5 more.  16 heads over 32,768 keys in fp16 24 us (floor 11), 8
-// ragged requests of up to 8,191 keys 19 (6), 16 heads over 2,300 in fp32 10.0 (0.9).
+// ragged requests of up to 8,191 keys 19 (6), 16 heads over 2,300 in fp32 10.3 (0.9).
 constexpr int TP = 32;        // positions per tile = one warp's step
 // Six warps with two tiles each and two CTAs per SM: 60 to 120 KB in flight per SM.  8 x 2 tiles
 // took 10.4 us for 9.9 (16 heads over 2,300 keys, fp32) and 24.9 for 23.5 (32,768 keys, fp16);
@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
     // Off, of standard normal keys and values: 6e-5 of the result at 2,300 without the three,
     // 8e-6 without the second, 2e-7 with both; at 65,536 8e-6 without the third, 3e-7 with it: no
     // more than plain fp32 sums.  They took 2,300 keys from 9.9 to 10.6 us (10.0 since a warp's
-    // sums have memory of their own).
+    // sums have memory of their own).  The low parts of q have sums of their own, else each of
+    // their products is cut at the large ones' sum: 1.7e-6 -> 8e-7 off with keys whose channels
+    // differ tenfold, for 0.3 us.
     constexpr bool FINE = T == KV4_F32;
     extern __shared__ __align__(128) uint8_t smem[];
     AttnShared<D, NG, MODE>& S = *reinterpret_cast<AttnShared<D, NG, MODE>*>(smem);
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
             }
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-                float acc[2][NT][4];
+                float acc[2][NT][4], low[2][4];      // FINE: products of q's low parts in sums of their own
 #pragma unroll
                 for (int j = 0; j < BPG; ++j) {
                     const int i2 = gi * BPG + j;
@@ -955,11 +957,21 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(MODE, D)) kv4_attention_k
                             else mma16816(acc[hh][nt], a0, qf[nt].x, qf[nt].y);
                             mma16816(acc[hh][nt], a1, qf[nt].z, qf[nt].w);
                         }
-                        if (MODE == HL8) {
+                        if (FINE) {
+                            if (j == 0) mma16816_0(low[hh], a0, ql.x, ql.y);
+                            else mma16816(low[hh], a0, ql.x, ql.y);
+                            mma16816(low[hh], a1, ql.z, ql.w);
+                        } else if (MODE == HL8) {
                             mma16816(acc[hh][0], a0, ql.x, ql.y);
                             mma16816(acc[hh][0], a1, ql.z, ql.w);
                         }
                     }
+                }
+                if (FINE) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[hh][0][k] += low[hh][k];
                 }
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
